@@ -408,6 +408,69 @@ int moe_cluster_partition(const void *F, int32_t d, int32_t d_ff, int32_t E, int
 int moe_cluster_distances(const void *F, int32_t d, int32_t d_ff, int32_t E, int32_t dtype,
                           const double *centers, double *D, void *stream);
 
+/* ---- microscaled 4-bit experts (mx4) ---------------------------------------
+ * The expert weights, and optionally the rows they are multiplied with, in the
+ * OCP microscaling format MXFP4 [OCP Microscaling Formats (MX) Specification
+ * v1.0, sections 5.1-5.3, 6.3]: 4-bit e2m1 elements (0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * a sign bit) with one e8m0 scale per block of 32 columns.  For a block v:
+ *     a = max |v_i|,  s = max(floor(log2 a) - 2, -127),
+ *     q_i = v_i 2^-s rounded to the nearest e2m1 value (ties to even, at most 6),
+ *     and the stored value is q_i 2^s.
+ * A block of zeros has s = -127; a block that holds a NaN or an infinity has scale
+ * byte 255 and codes 0, and every element of it reads as NaN.
+ *
+ * An mx4 matrix batch [G][rows][K] is two buffers (K32 = K rounded up to 32):
+ *   codes  [G][rows][K32/2] bytes; column c is bits 4(c%2)..4(c%2)+3 of byte c/2
+ *          (bit 3 of a code is the sign); columns K..K32 are zero codes;
+ *   scales [G][ceil(rows/128)][ceil(K/128)] tiles of 512 bytes, one byte s + 127 per
+ *          row and block: row r, block b at byte (r%32)*16 + (r%128)/32*4 + b%4 of
+ *          tile (r/128, b/4) -- the order the tensor cores take scales in.  Bytes of
+ *          rows and blocks past the matrix are zero.
+ * The packed expert weights keep their row order: W13_q / W13_s is the batch
+ * [E][2*m16][d] of W13_e, W2_q / W2_s the batch [E][d][m8] of W2_e.
+ *
+ * Rows grouped by expert (x_q / x_s, h_q / h_s): codes [T*k][K32/2], row r as in
+ * x_perm; scales in tiles of the same form, the tiles of expert e starting at tile
+ * row offsets[e]/128 + e, so that row r of expert e is row (r - offsets[e]) % 128 of
+ * tile row offsets[e]/128 + e + (r - offsets[e])/128.  Bytes past an expert's rows
+ * are never read as values.
+ *
+ * mx4 calls take bf16 layers (f32 too in moe_mx4_quantize / _dequantize /
+ * _dispatch) with d a multiple of 32 (MOE_ERR_SHAPE otherwise). */
+
+/* Bytes of the codes and scales of a batch [G][rows][K]; 0 if an argument is < 1 or
+ * K is no multiple of 8.  Host-only. */
+size_t moe_mx4_codes_bytes(int32_t G, int32_t rows, int32_t K);
+size_t moe_mx4_scales_bytes(int32_t G, int32_t rows, int32_t K);
+
+/* Bytes of the codes and scales of the T*k expert rows of K columns (K = p->d for
+ * x_q / x_s, p->m for h_q / h_s; at least one row's worth, so that the buffers
+ * of an empty batch are not empty); 0 on bad params.  Host-only. */
+size_t moe_mx4_rows_bytes(const moe_params_t *p, int32_t K);
+size_t moe_mx4_row_scales_bytes(const moe_params_t *p, int32_t K);
+
+/* Quantises src [G][rows][K] (dtype MOE_BF16 or MOE_F32; rows ld elements apart,
+ * matrices rows*ld apart) into codes and scales; every byte of both is written.
+ * K and ld multiples of 8, ld >= K.  Exact: the result is that of the formula above.
+ * Errors: MOE_ERR_INVALID_ARG (NULL, G or rows < 1), MOE_ERR_SHAPE, MOE_ERR_DTYPE,
+ * MOE_ERR_ALIGN, MOE_ERR_CUDA. */
+int moe_mx4_quantize(const void *src, int32_t dtype, int32_t G, int32_t rows, int32_t K,
+                     int64_t ld, void *codes, void *scales, void *stream);
+
+/* The values of an mx4 batch, q 2^s, into dst [G][rows][K] (dtype; rows ld elements
+ * apart, columns K..ld untouched).  Every finite mx4 value below 2^127 is a bf16
+ * value: nothing is rounded.  Errors as moe_mx4_quantize. */
+int moe_mx4_dequantize(const void *codes, const void *scales, int32_t dtype, int32_t G,
+                       int32_t rows, int32_t K, int64_t ld, void *dst, void *stream);
+
+/* a2's row copy in mx4: quantises every token row of x [T][d] (dtype of p) once and
+ * writes it to each row its kept assignments own: x_q, x_s in the layout above.
+ * topk_idx, slot_row and offsets are moe_dispatch_rows' outputs (a slot of -1, or an
+ * expert outside [0,E), is skipped). */
+int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_idx,
+                     const int32_t *slot_row, const int32_t *offsets, void *x_q, void *x_s,
+                     void *stream);
+
 /* ---- backward of the layer (bf16 layers, T >= 1) ---------------------------
  * Gradients of l(y) + c * L_balance for a scalar loss l, given dy = dl/dy and c
  * (dLb below); the chain rule of each forward step ("Llama 3 Meets MoE",

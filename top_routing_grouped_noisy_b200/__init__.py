@@ -31,6 +31,9 @@ __all__ = [
     "moe_route_backward", "moe_backward", "BackwardBuffers",
     "moe_backward_residual_workspace_size", "moe_backward_residual", "EpPlan", "moe_ep_plan",
     "moe_ep_mask_slots", "moe_ep_gate_stats", "EP_CAPACITY_GLOBAL", "EP_CAPACITY_LOCAL",
+    "moe_mx4_codes_bytes", "moe_mx4_scales_bytes", "moe_mx4_rows_bytes",
+    "moe_mx4_row_scales_bytes", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_dispatch",
+    "Mx4Experts",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -152,6 +155,13 @@ def lib():
             "moe_ep_plan": (C.c_int, [v, i32, i32, i32, i32, i32, v, v, v, v, v, v]),
             "moe_ep_mask_slots": (C.c_int, [P, v, v, v, v, v]),
             "moe_ep_gate_stats": (C.c_int, [P, v, i32, v, v, v, v, v, v]),
+            "moe_mx4_codes_bytes": (sz, [i32, i32, i32]),
+            "moe_mx4_scales_bytes": (sz, [i32, i32, i32]),
+            "moe_mx4_rows_bytes": (sz, [P, i32]),
+            "moe_mx4_row_scales_bytes": (sz, [P, i32]),
+            "moe_mx4_quantize": (C.c_int, [v, i32, i32, i32, i32, i64, v, v, v]),
+            "moe_mx4_dequantize": (C.c_int, [v, v, i32, i32, i32, i32, i64, v, v]),
+            "moe_mx4_dispatch": (C.c_int, [P, v, v, v, v, v, v, v]),
             "moe_pipeline_create": (C.c_int, [P, v, v, v, v, v, i32, C.POINTER(v)]),
             "moe_pipeline_submit": (C.c_int, [v, v, v, v, v, C.POINTER(i64)]),
             "moe_pipeline_wait": (C.c_int, [v, i64]),
@@ -239,13 +249,19 @@ def moe_workspace_size(p: Params) -> int:
 
 
 class Workspace:
-    """Caller-owned scratch for the library (a zeroed torch uint8 buffer)."""
+    """Caller-owned scratch for the library (a zeroed torch uint8 buffer): a new one, or
+    ``buf``, a CUDA uint8 tensor of at least moe_workspace_size(p) bytes, which is zeroed."""
 
-    def __init__(self, p: Params, device=None, nbytes=None):
+    def __init__(self, p: Params, device=None, nbytes=None, buf=None):
         n = nbytes if nbytes is not None else moe_workspace_size(p)
         if n <= 0:
             raise MoeError(MOE_ERR_INVALID_ARG, "invalid parameters for the workspace")
-        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        if buf is not None:
+            if buf.dtype != torch.uint8 or buf.numel() < n:
+                raise MoeError(MOE_ERR_WORKSPACE, "the workspace needs %d uint8 elements" % n)
+            n = buf.numel()
+        self.buf = buf if buf is not None else torch.empty(n, dtype=torch.uint8,
+                                                           device=device or "cuda")
         self.nbytes = n
         _check(lib().moe_workspace_init(_p(self.buf), n, _stream()))
 
@@ -696,3 +712,95 @@ def moe_backward_residual(p, x, Wg, W13_e, W2_e, W13_s, W2_s, m_s, h_s, fwd: "Fo
                                        int(m_s), _p(h_s), _p(dh_s), _p(dx_s), _p(dW13_s),
                                        _p(dW2_s), float(dLb), ws.ptr, ws.nbytes, _stream(stream)))
     return g
+
+
+# --------------------------------------------------------------------------- mx4
+
+def moe_mx4_codes_bytes(G, rows, K) -> int:
+    return int(lib().moe_mx4_codes_bytes(G, rows, K))
+
+
+def moe_mx4_scales_bytes(G, rows, K) -> int:
+    return int(lib().moe_mx4_scales_bytes(G, rows, K))
+
+
+def moe_mx4_rows_bytes(p, K) -> int:
+    return int(lib().moe_mx4_rows_bytes(C.byref(p), K))
+
+
+def moe_mx4_row_scales_bytes(p, K) -> int:
+    return int(lib().moe_mx4_row_scales_bytes(C.byref(p), K))
+
+
+def _mx4_rows(t):
+    """(pointer, G, rows, K, ld) of a matrix or batch of matrices whose columns are
+    contiguous and whose rows are evenly spaced through the batch."""
+    if t.dim() not in (2, 3):
+        raise ValueError("expected [rows][K] or [G][rows][K], got %d dimensions" % t.dim())
+    b = t if t.dim() == 3 else t.unsqueeze(0)
+    G, rows, K = b.shape
+    ld = b.stride(1) if rows > 1 else (b.stride(0) if G > 1 else K)
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors (got a %s tensor)" % t.device)
+    if b.stride(2) != 1 or (G > 1 and b.stride(0) != rows * ld):
+        raise ValueError("the rows of the matrices must be contiguous and evenly spaced")
+    return t.data_ptr() or None, G, rows, K, ld
+
+
+def _mx4_bytes(t, n, name):
+    if t.dtype != torch.uint8 or t.numel() != n:
+        raise ValueError("%s must hold %d uint8 elements" % (name, n))
+    return _p(t)
+
+
+def moe_mx4_quantize(src, out=None, stream=None):
+    """src [rows][K] or [G][rows][K] (bf16 or f32; rows may be spaced) in mx4: (codes
+    [G][rows][K32/2], scales [G][rows/128][K/128][32][4][4]) uint8 (include/moe.h)."""
+    ptr, G, rows, K, ld = _mx4_rows(src)
+    if out is None:
+        u8 = dict(dtype=torch.uint8, device=src.device)
+        out = (torch.empty(G, rows, (K + 31) // 32 * 16, **u8),
+               torch.empty(G, (rows + 127) // 128, (K + 127) // 128, 32, 4, 4, **u8))
+    codes, scales = out
+    _check(lib().moe_mx4_quantize(ptr, _dtype_code(src.dtype), G, rows, K, ld,
+                                  _mx4_bytes(codes, moe_mx4_codes_bytes(G, rows, K), "codes"),
+                                  _mx4_bytes(scales, moe_mx4_scales_bytes(G, rows, K), "scales"),
+                                  _stream(stream)))
+    return out
+
+
+def moe_mx4_dequantize(codes, scales, K, dtype=torch.bfloat16, out=None, stream=None):
+    """The values [G][rows][K] of an mx4 batch (codes [G][rows][K32/2] as moe_mx4_quantize
+    gives them); with ``out`` its dtype and row spacing count."""
+    G, rows = codes.shape[0], codes.shape[1]
+    if out is None:
+        out = torch.empty(G, rows, K, dtype=dtype, device=codes.device)
+    ptr, Go, ro, Ko, ld = _mx4_rows(out)
+    if (Go, ro, Ko) != (G, rows, K):
+        raise ValueError("out must be [%d][%d][%d]" % (G, rows, K))
+    _check(lib().moe_mx4_dequantize(_mx4_bytes(codes, moe_mx4_codes_bytes(G, rows, K), "codes"),
+                                    _mx4_bytes(scales, moe_mx4_scales_bytes(G, rows, K), "scales"),
+                                    _dtype_code(out.dtype), G, rows, K, ld, ptr,
+                                    _stream(stream)))
+    return out
+
+
+class Mx4Experts:
+    """The packed expert weights of a layer in mx4: W13_q / W13_s of W13_e [E][2*m16][d] and
+    W2_q / W2_s of W2_e [E][d][m8]."""
+
+    def __init__(self, W13_q, W13_s, W2_q, W2_s):
+        self.W13_q, self.W13_s, self.W2_q, self.W2_s = W13_q, W13_s, W2_q, W2_s
+
+    @classmethod
+    def quantize(cls, W13_e, W2_e, E, m, d, stream=None):
+        """From the packed weights of moe_partition_experts (bf16 or f32)."""
+        m16, m8 = (m + 15) // 16 * 16, (m + 7) // 8 * 8
+        return cls(*moe_mx4_quantize(W13_e.view(E, 2 * m16, d), stream=stream),
+                   *moe_mx4_quantize(W2_e.view(E, d, m8), stream=stream))
+
+
+def moe_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s, stream=None):
+    """a2's row copy in mx4 (after moe_dispatch_rows)."""
+    _check(lib().moe_mx4_dispatch(C.byref(p), _p(x), _p(topk_idx), _p(slot_row), _p(offsets),
+                                  _p(x_q), _p(x_s), _stream(stream)))

@@ -183,4 +183,13 @@ cudaError_t launch_gate_stats(const moe_params_t *p, const int32_t *counts,
                               const float *probs_sum, float *f, float *P, float *loss,
                               cudaStream_t s);
 
+// mx4 (include/moe.h, microscaled 4-bit experts)
+cudaError_t launch_mx4_quantize(const void *src, int dtype, int G, int rows, int K, int64_t ld,
+                                void *codes, void *scales, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const void *codes, const void *scales, int dtype, int G,
+                                  int rows, int K, int64_t ld, void *dst, cudaStream_t s);
+cudaError_t launch_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *idx,
+                                const int32_t *slot, const int32_t *offsets, void *xq, void *xs,
+                                cudaStream_t s);
+
 }  // namespace moe

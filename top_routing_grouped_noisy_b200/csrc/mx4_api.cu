@@ -1,0 +1,161 @@
+// mx4_api.cu -- the extern "C" entry points of the microscaled 4-bit (mx4) calls:
+// argument validation and launch sequences.
+#include <cstdio>
+
+#include "mx4.cuh"
+
+namespace moe {
+namespace {
+
+int mx_fail(int code, const char *fn, const char *what)
+{
+    char msg[256];
+    snprintf(msg, sizeof msg, "%s: %s", fn, what);
+    return report_error(code, msg);
+}
+
+// a required device pointer: not NULL, 16-byte aligned
+int mx_ptr(const char *fn, const void *ptr, const char *name)
+{
+    char msg[128];
+    if (ptr == nullptr) {
+        snprintf(msg, sizeof msg, "argument '%s' is NULL", name);
+        return mx_fail(MOE_ERR_INVALID_ARG, fn, msg);
+    }
+    if ((reinterpret_cast<uintptr_t>(ptr) & 15u) != 0) {
+        snprintf(msg, sizeof msg, "argument '%s' is not 16-byte aligned", name);
+        return mx_fail(MOE_ERR_ALIGN, fn, msg);
+    }
+    return MOE_OK;
+}
+
+#define MX_PTR(ptr)                                       \
+    do {                                                  \
+        const int rc_ = mx_ptr(fn, (ptr), #ptr);          \
+        if (rc_ != MOE_OK)                                \
+            return rc_;                                   \
+    } while (0)
+
+// Token-sized buffers may be NULL when the batch is empty (T == 0).
+#define MX_TOK(ptr)                                       \
+    do {                                                  \
+        if (p->T > 0 || (ptr) != nullptr)                 \
+            MX_PTR(ptr);                                  \
+    } while (0)
+
+int mx_after(const char *fn, cudaError_t e)
+{
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    return e == cudaSuccess ? report_ok() : report_cuda(e, fn);
+}
+
+// the layer as the mx4 calls take it
+int mx_params(const char *fn, const moe_params_t *p)
+{
+    const int rc = validate_params(fn, p);
+    if (rc != MOE_OK)
+        return rc;
+    if (p->d % kMx4Block != 0)
+        return mx_fail(MOE_ERR_SHAPE, fn, "d is not a multiple of 32");
+    return MOE_OK;
+}
+
+int mx_matrix(const char *fn, int32_t dtype, int32_t G, int32_t rows, int32_t K, int64_t ld)
+{
+    if (dtype != MOE_BF16 && dtype != MOE_F32)
+        return mx_fail(MOE_ERR_DTYPE, fn, "dtype is neither MOE_BF16 nor MOE_F32");
+    if (G < 1 || rows < 1)
+        return mx_fail(MOE_ERR_INVALID_ARG, fn, "G or rows is below 1");
+    if (K < 8 || K % 8 != 0 || K > 1 << 22 || rows > 1 << 28)
+        return mx_fail(MOE_ERR_SHAPE, fn, "K is not a positive multiple of 8, or too large");
+    if (ld < K || ld % 8 != 0)
+        return mx_fail(MOE_ERR_SHAPE, fn, "ld is below K or not a multiple of 8");
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_mx4_codes_bytes(int32_t G, int32_t rows, int32_t K)
+{
+    if (G < 1 || rows < 1 || K < 8 || K % 8 != 0)
+        return 0;
+    return (size_t)G * rows * (mx4_k32(K) / 2);
+}
+
+size_t moe_mx4_scales_bytes(int32_t G, int32_t rows, int32_t K)
+{
+    if (G < 1 || rows < 1 || K < 8 || K % 8 != 0)
+        return 0;
+    return (size_t)G * ((rows + 127) / 128) * ((K + 127) / 128) * kMx4Tile;
+}
+
+size_t moe_mx4_rows_bytes(const moe_params_t *p, int32_t K)
+{
+    if (validate_params("moe_mx4_rows_bytes", p) != MOE_OK || K < 1)
+        return 0;
+    const size_t rows = (size_t)p->T * p->k;
+    return (rows > 0 ? rows : 1) * (mx4_k32(K) / 2);
+}
+
+size_t moe_mx4_row_scales_bytes(const moe_params_t *p, int32_t K)
+{
+    if (validate_params("moe_mx4_row_scales_bytes", p) != MOE_OK || K < 1)
+        return 0;
+    return (size_t)mx4_row_tiles((int64_t)p->T * p->k, p->E) * ((K + 127) / 128) * kMx4Tile;
+}
+
+int moe_mx4_quantize(const void *src, int32_t dtype, int32_t G, int32_t rows, int32_t K,
+                     int64_t ld, void *codes, void *scales, void *stream)
+{
+    const char *fn = "moe_mx4_quantize";
+    const int rc = mx_matrix(fn, dtype, G, rows, K, ld);
+    if (rc != MOE_OK)
+        return rc;
+    MX_PTR(src);
+    MX_PTR(codes);
+    MX_PTR(scales);
+    return mx_after(fn, launch_mx4_quantize(src, dtype, G, rows, K, ld, codes, scales,
+                                            (cudaStream_t)stream));
+}
+
+int moe_mx4_dequantize(const void *codes, const void *scales, int32_t dtype, int32_t G,
+                       int32_t rows, int32_t K, int64_t ld, void *dst, void *stream)
+{
+    const char *fn = "moe_mx4_dequantize";
+    const int rc = mx_matrix(fn, dtype, G, rows, K, ld);
+    if (rc != MOE_OK)
+        return rc;
+    MX_PTR(codes);
+    MX_PTR(scales);
+    MX_PTR(dst);
+    return mx_after(fn, launch_mx4_dequantize(codes, scales, dtype, G, rows, K, ld, dst,
+                                              (cudaStream_t)stream));
+}
+
+int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_idx,
+                     const int32_t *slot_row, const int32_t *offsets, void *x_q, void *x_s,
+                     void *stream)
+{
+    const char *fn = "moe_mx4_dispatch";
+    const int rc = mx_params(fn, p);
+    if (rc != MOE_OK)
+        return rc;
+    MX_TOK(x);
+    MX_TOK(topk_idx);
+    MX_TOK(slot_row);
+    MX_PTR(offsets);
+    MX_TOK(x_q);
+    MX_TOK(x_s);
+    if (p->T == 0)
+        return report_ok();
+    return mx_after(fn, launch_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s,
+                                            (cudaStream_t)stream));
+}
+
+}  // extern "C"
