@@ -471,6 +471,26 @@ int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_i
                      const int32_t *slot_row, const int32_t *offsets, void *x_q, void *x_s,
                      void *stream);
 
+/* a3 on mx4 operands: h = silu(xq W1_e^T) * (xq W3_e^T) for the kept rows, where xq are
+ * the values of x_q / x_s, accumulated in f32 by block-scaled tcgen05 products; h is
+ * quantised from f32 into h_q / h_s (blocks of 32 neurons; neurons >= m are zeros).
+ * Rows past offsets[E] are left as they were. */
+int moe_expert_up_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
+                      const int32_t *offsets, const void *W13_q, const void *W13_s, void *h_q,
+                      void *h_s, void *ws, size_t ws_bytes, void *stream);
+
+/* a4 on mx4 operands: out[r] = hq[r] W2_e^T, accumulated in f32, rounded to bf16.
+ * out [T*k][d]; rows past offsets[E] are left as they were. */
+int moe_expert_down_mx4(const moe_params_t *p, const void *h_q, const void *h_s,
+                        const int32_t *offsets, const void *W2_q, const void *W2_s, void *out,
+                        void *ws, size_t ws_bytes, void *stream);
+
+/* a3 then a4. */
+int moe_expert_ffn_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
+                       const int32_t *offsets, const void *W13_q, const void *W13_s,
+                       const void *W2_q, const void *W2_s, void *h_q, void *h_s, void *out,
+                       void *ws, size_t ws_bytes, void *stream);
+
 /* ---- backward of the layer (bf16 layers, T >= 1) ---------------------------
  * Gradients of l(y) + c * L_balance for a scalar loss l, given dy = dl/dy and c
  * (dLb below); the chain rule of each forward step ("Llama 3 Meets MoE",

@@ -109,3 +109,30 @@ def test_expert_tiles_do_not_overlap(seed):
         assert first >= end
         end = first + -(-int(n[e]) // 128)
     assert end <= off[-1] // 128 + E + 1
+
+
+def test_expert_refusals(L):
+    p = moe.params(16, 64, 8, 2, 16)
+    n = moe.moe_workspace_size(p)
+    ws = _fake(20)
+    calls = {
+        "up": (L.moe_expert_up_mx4, 7, {0: "x_q", 3: "W13_q", 6: "h_s"}),
+        "down": (L.moe_expert_down_mx4, 6, {1: "h_s", 4: "W2_s", 5: "out"}),
+        "ffn": (L.moe_expert_ffn_mx4, 10, {2: "offsets", 6: "W2_s", 9: "out"}),
+    }
+    for fn, count, names in calls.values():
+        f = [_fake(i) for i in range(count)]
+        assert fn(None, *f, ws, n, None) == moe.MOE_ERR_INVALID_ARG
+        assert fn(C.byref(moe.params(16, 72, 8, 2, 16)), *f, ws, n, None) == moe.MOE_ERR_SHAPE
+        f32 = moe.params(16, 64, 8, 2, 16, dtype=moe.MOE_F32)
+        assert fn(C.byref(f32), *f, ws, 1 << 24, None) == moe.MOE_ERR_DTYPE
+        assert fn(C.byref(p), *f, None, n, None) == moe.MOE_ERR_INVALID_ARG
+        assert fn(C.byref(p), *f, ws, n - 1, None) == moe.MOE_ERR_WORKSPACE
+        for i in range(count):
+            a = list(f)
+            a[i] = None
+            assert fn(C.byref(p), *a, ws, n, None) == moe.MOE_ERR_INVALID_ARG
+            if i in names:
+                assert ("'%s'" % names[i]).encode() in L.moe_last_error_string()
+            a[i] = _fake(i, 8)
+            assert fn(C.byref(p), *a, ws, n, None) == moe.MOE_ERR_ALIGN

@@ -33,7 +33,7 @@ __all__ = [
     "moe_ep_mask_slots", "moe_ep_gate_stats", "EP_CAPACITY_GLOBAL", "EP_CAPACITY_LOCAL",
     "moe_mx4_codes_bytes", "moe_mx4_scales_bytes", "moe_mx4_rows_bytes",
     "moe_mx4_row_scales_bytes", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_dispatch",
-    "Mx4Experts",
+    "moe_expert_up_mx4", "moe_expert_down_mx4", "moe_expert_ffn_mx4", "Mx4Experts",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -162,6 +162,9 @@ def lib():
             "moe_mx4_quantize": (C.c_int, [v, i32, i32, i32, i32, i64, v, v, v]),
             "moe_mx4_dequantize": (C.c_int, [v, v, i32, i32, i32, i32, i64, v, v]),
             "moe_mx4_dispatch": (C.c_int, [P, v, v, v, v, v, v, v]),
+            "moe_expert_up_mx4": (C.c_int, [P, v, v, v, v, v, v, v, v, sz, v]),
+            "moe_expert_down_mx4": (C.c_int, [P, v, v, v, v, v, v, v, sz, v]),
+            "moe_expert_ffn_mx4": (C.c_int, [P, v, v, v, v, v, v, v, v, v, v, v, sz, v]),
             "moe_pipeline_create": (C.c_int, [P, v, v, v, v, v, i32, C.POINTER(v)]),
             "moe_pipeline_submit": (C.c_int, [v, v, v, v, v, C.POINTER(i64)]),
             "moe_pipeline_wait": (C.c_int, [v, i64]),
@@ -804,3 +807,20 @@ def moe_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s, stream=None):
     """a2's row copy in mx4 (after moe_dispatch_rows)."""
     _check(lib().moe_mx4_dispatch(C.byref(p), _p(x), _p(topk_idx), _p(slot_row), _p(offsets),
                                   _p(x_q), _p(x_s), _stream(stream)))
+
+
+def moe_expert_up_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, ws, stream=None):
+    _check(lib().moe_expert_up_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets), _p(W.W13_q),
+                                   _p(W.W13_s), _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
+                                   _stream(stream)))
+
+
+def moe_expert_down_mx4(p, h_q, h_s, offsets, W: Mx4Experts, out, ws, stream=None):
+    _check(lib().moe_expert_down_mx4(C.byref(p), _p(h_q), _p(h_s), _p(offsets), _p(W.W2_q),
+                                     _p(W.W2_s), _p(out), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def moe_expert_ffn_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, out, ws, stream=None):
+    _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets), _p(W.W13_q),
+                                    _p(W.W13_s), _p(W.W2_q), _p(W.W2_s), _p(h_q), _p(h_s),
+                                    _p(out), ws.ptr, ws.nbytes, _stream(stream)))

@@ -192,4 +192,11 @@ cudaError_t launch_mx4_dispatch(const moe_params_t *p, const void *x, const int3
                                 const int32_t *slot, const int32_t *offsets, void *xq, void *xs,
                                 cudaStream_t s);
 
+cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
+                          const int32_t *offsets, const void *W13q, const void *W13s, void *hq,
+                          void *hs, int32_t *status, cudaStream_t s);
+cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *hs,
+                            const int32_t *offsets, const void *W2q, const void *W2s, void *out,
+                            int32_t *status, cudaStream_t s);
+
 }  // namespace moe

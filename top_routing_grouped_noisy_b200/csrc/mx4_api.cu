@@ -61,6 +61,21 @@ int mx_params(const char *fn, const moe_params_t *p)
     return MOE_OK;
 }
 
+// a bf16 layer and its workspace (`tensor core` calls)
+int mx_layer(const char *fn, const moe_params_t *p, void *ws, size_t ws_bytes)
+{
+    const int rc = mx_params(fn, p);
+    if (rc != MOE_OK)
+        return rc;
+    if (p->dtype != MOE_BF16)
+        return mx_fail(MOE_ERR_DTYPE, fn, "the mx4 experts are bf16 layers");
+    if (mx_ptr(fn, ws, "ws") != MOE_OK)
+        return mx_ptr(fn, ws, "ws");
+    if (ws_bytes < ws_layout(p).total)
+        return mx_fail(MOE_ERR_WORKSPACE, fn, "the workspace is below moe_workspace_size");
+    return MOE_OK;
+}
+
 int mx_matrix(const char *fn, int32_t dtype, int32_t G, int32_t rows, int32_t K, int64_t ld)
 {
     if (dtype != MOE_BF16 && dtype != MOE_F32)
@@ -156,6 +171,65 @@ int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_i
         return report_ok();
     return mx_after(fn, launch_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s,
                                             (cudaStream_t)stream));
+}
+
+int moe_expert_up_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
+                      const int32_t *offsets, const void *W13_q, const void *W13_s, void *h_q,
+                      void *h_s, void *ws, size_t ws_bytes, void *stream)
+{
+    const char *fn = "moe_expert_up_mx4";
+    const int rc = mx_layer(fn, p, ws, ws_bytes);
+    if (rc != MOE_OK)
+        return rc;
+    MX_TOK(x_q);
+    MX_TOK(x_s);
+    MX_PTR(offsets);
+    MX_PTR(W13_q);
+    MX_PTR(W13_s);
+    MX_TOK(h_q);
+    MX_TOK(h_s);
+    if (p->T == 0)
+        return report_ok();
+    return mx_after(fn, launch_mx4_up(p, x_q, x_s, offsets, W13_q, W13_s, h_q, h_s,
+                                      reinterpret_cast<int32_t *>(ws), (cudaStream_t)stream));
+}
+
+int moe_expert_down_mx4(const moe_params_t *p, const void *h_q, const void *h_s,
+                        const int32_t *offsets, const void *W2_q, const void *W2_s, void *out,
+                        void *ws, size_t ws_bytes, void *stream)
+{
+    const char *fn = "moe_expert_down_mx4";
+    const int rc = mx_layer(fn, p, ws, ws_bytes);
+    if (rc != MOE_OK)
+        return rc;
+    MX_TOK(h_q);
+    MX_TOK(h_s);
+    MX_PTR(offsets);
+    MX_PTR(W2_q);
+    MX_PTR(W2_s);
+    MX_TOK(out);
+    if (p->T == 0)
+        return report_ok();
+    return mx_after(fn, launch_mx4_down(p, h_q, h_s, offsets, W2_q, W2_s, out,
+                                        reinterpret_cast<int32_t *>(ws), (cudaStream_t)stream));
+}
+
+int moe_expert_ffn_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
+                       const int32_t *offsets, const void *W13_q, const void *W13_s,
+                       const void *W2_q, const void *W2_s, void *h_q, void *h_s, void *out,
+                       void *ws, size_t ws_bytes, void *stream)
+{
+    const char *fn = "moe_expert_ffn_mx4";
+    int rc = mx_layer(fn, p, ws, ws_bytes);
+    if (rc != MOE_OK)
+        return rc;
+    MX_PTR(W2_q);  // the second half's arguments before the first half is launched
+    MX_PTR(W2_s);
+    MX_TOK(out);
+    if ((rc = moe_expert_up_mx4(p, x_q, x_s, offsets, W13_q, W13_s, h_q, h_s, ws, ws_bytes,
+                                stream)) != MOE_OK)
+        return rc;
+    return moe_expert_down_mx4(p, h_q, h_s, offsets, W2_q, W2_s, out, ws, ws_bytes, stream);
 }
 
 }  // extern "C"
