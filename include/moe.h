@@ -491,6 +491,58 @@ int moe_expert_ffn_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
                        const void *W2_q, const void *W2_s, void *h_q, void *h_s, void *out,
                        void *ws, size_t ws_bytes, void *stream);
 
+/* How moe_forward_mx4 takes the activations. */
+enum {
+    MOE_MX4_ACT_BF16 = 0, /* weights mx4 only: x and h stay bf16; batches of 1..16 tokens */
+    MOE_MX4_ACT_MX4 = 1   /* rows and h quantised as in moe_expert_ffn_mx4; any T */
+};
+#define MOE_MX4_FEW_TOKENS 16
+
+/* Every buffer moe_forward_mx4 touches (device pointers, caller-owned). */
+typedef struct {
+    /* inputs */
+    const void *x;             /* [T][d] bf16 */
+    const void *Wg;            /* [d][E] bf16 */
+    const void *Wnoise;        /* [d][E] bf16 or NULL */
+    const float *noise;        /* [T][E] or NULL */
+    const float *bias;         /* [E] or NULL */
+    const void *W13_q, *W13_s; /* mx4 of W13_e */
+    const void *W2_q, *W2_s;   /* mx4 of W2_e */
+    const void *router_packed; /* moe_router_pack output or NULL */
+    /* outputs */
+    void *y;                   /* [T][d] bf16 */
+    float *loss;               /* [1] */
+    int32_t *counts;           /* [E] */
+    float *importance;         /* [E] */
+    float *f;                  /* [E] */
+    float *P;                  /* [E] */
+    /* intermediates (kept for inspection) */
+    int32_t *topk_idx;         /* [T][k] */
+    float *topk_w;             /* [T][k] */
+    float *probs_sum;          /* [E] */
+    int32_t *row_token;        /* [T*k] */
+    int32_t *slot_row;         /* [T][k] */
+    int32_t *kept;             /* [E] */
+    int32_t *offsets;          /* [E+1] */
+    void *h;                   /* [T*k][m8] bf16          ACT_BF16 (else unused, may be NULL) */
+    void *x_q, *x_s, *h_q, *h_s; /* expert rows in mx4    ACT_MX4 (else unused, may be NULL) */
+    void *out;                 /* [T*k][d] bf16           ACT_MX4 (else unused, may be NULL) */
+} moe_mx4_buffers_t;
+
+/* The whole layer (a1 .. a6) on mx4 expert weights, on one stream without host
+ * synchronisation.  Routing, dispatch, combine and statistics are those of
+ * moe_forward.
+ *   ACT_BF16: 1 <= T <= MOE_MX4_FEW_TOKENS.  One cooperative launch: the weights are
+ *     read once as mx4 and multiplied with the bf16 rows, f32 accumulation; h is
+ *     rounded to bf16, the expert outputs stay f32 until y is rounded.  Needs
+ *     E <= 32 (16 with noise); MOE_ERR_UNSUPPORTED for more experts or tokens.  T = 0
+ *     takes the steps of ACT_MX4.
+ *   ACT_MX4: moe_route, moe_dispatch_rows, moe_mx4_dispatch, moe_expert_ffn_mx4,
+ *     moe_combine, moe_gate_stats.
+ * Errors: as moe_forward; MOE_ERR_DTYPE unless bf16; MOE_ERR_INVALID_ARG for act. */
+int moe_forward_mx4(const moe_params_t *p, const moe_mx4_buffers_t *b, int32_t act, void *ws,
+                    size_t ws_bytes, void *stream);
+
 /* ---- backward of the layer (bf16 layers, T >= 1) ---------------------------
  * Gradients of l(y) + c * L_balance for a scalar loss l, given dy = dl/dy and c
  * (dLb below); the chain rule of each forward step ("Llama 3 Meets MoE",

@@ -278,3 +278,188 @@ def test_expert_ffn(T, E, k, m, d, cap):
     moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q, rt.h_s, rt.out, rt.ws)
     assert torch.equal(rt.out, out)
     assert moe.moe_get_device_status(rt.ws) == 0
+
+
+# --------------------------------------------------------------------------- the layer
+import types  # noqa: E402
+
+import harness as H  # noqa: E402
+
+
+class _Layer:
+    def __init__(self, T, E, k, m, d, noisy=False, router=moe.MIXTRAL, cap=-1, rescale=True,
+                 bias=False, seed=0):
+        g = torch.Generator().manual_seed(1000 + seed + 17 * T + d)
+        self.w = types.SimpleNamespace(T=T, E=E, k=k, m=m, d=d, router=router, lam=0.01)
+        r = lambda *s: torch.randn(*s, generator=g)
+        self.inp = {"x": r(T, d).bfloat16(), "Wg": (r(d, E) * 0.05).bfloat16(),
+                    "Wnoise": (r(d, E) * 0.05).bfloat16() if noisy else None,
+                    "eps": r(T, E) if noisy else None, "bias": r(E) if bias else None}
+        self.W, self.w1, self.w3, self.w2 = _experts(E, m, d, seed + T + d)
+        self.p = moe.params(T, d, E, k, m, router_type=router, capacity=cap, rescale=rescale,
+                            balance_lambda=0.01)
+        self.ws = moe.Workspace(self.p)
+        self.dev = {n: None if v is None else v.cuda() for n, v in self.inp.items()}
+        self.scale = E / k if rescale else 1.0
+
+    def run(self, act, bufs=None, **kw):
+        bufs = moe.Mx4Buffers(self.p, act=act) if bufs is None else bufs
+        v = self.dev
+        moe.moe_forward_mx4(self.p, v["x"], v["Wg"], self.W, self.ws, bufs, act=act,
+                            Wnoise=v["Wnoise"], noise=v["eps"], bias=v["bias"], **kw)
+        return bufs
+
+    def check_tables(self, b):
+        """Routing against the oracle, the tables against a stable sort of the indices."""
+        r, _ = H.check_routing(self.w, self.inp, b, 5e-5)
+        import oracle
+        d = oracle.dispatch(b.topk_idx.cpu().numpy(), self.w.E, self.p.capacity)
+        for n in ("counts", "kept", "offsets", "slot_row"):
+            np.testing.assert_array_equal(getattr(b, n).cpu().numpy(), d[n])
+        np.testing.assert_array_equal(b.row_token.cpu().numpy()[: d["R"]], d["row_token"])
+        T, k = self.w.T, self.w.k
+        np.testing.assert_allclose(b.f.cpu().numpy(), d["counts"] / (T * k), rtol=1e-6)
+        np.testing.assert_allclose(b.P.cpu().numpy(), b.probs_sum.cpu().numpy() / T, rtol=1e-6)
+        H.check_loss(self.w, b, r)
+        return d
+
+    def combine(self, out, b, d):
+        """y from expert rows `out` and the kernel's own gate weights, and sum |.|."""
+        G, slot = mp.f64(b.topk_w), d["slot_row"]
+        rows = np.where((slot >= 0)[..., None], out[np.maximum(slot, 0)], 0.0) if len(out) else \
+            np.zeros((*slot.shape, self.w.d))
+        terms = self.scale * G[..., None] * rows
+        return terms.sum(1), np.abs(terms).sum(1)
+
+
+def _check_few(L, b):
+    d = L.check_tables(b)
+    w, off, R = L.w, d["offsets"], d["R"]
+    x = mp.f64(L.inp["x"])
+    h = mp.f64(b.h)[:R, : w.m]
+    out, mag = np.zeros((R, w.d)), np.zeros((R, w.d))
+    for e in range(w.E):
+        rows = slice(off[e], off[e + 1])
+        if off[e] == off[e + 1]:
+            continue
+        xs = x[d["row_token"][rows]]
+        g, u = xs @ L.w1[e].T, xs @ L.w3[e].T
+        # activations scaled into f16: off by at most 2^-38 of the row's maximum each
+        tiny = 2.0 ** -38 * np.abs(xs).max(1, keepdims=True)
+        eg = _acc_bound(w.d) * (np.abs(xs) @ np.abs(L.w1[e]).T) + tiny * np.abs(L.w1[e]).sum(1)
+        eu = _acc_bound(w.d) * (np.abs(xs) @ np.abs(L.w3[e]).T) + tiny * np.abs(L.w3[e]).sum(1)
+        s = g / (1 + np.exp(-g))
+        ref = s * u
+        tol = 1.1 * eg * np.abs(u) + np.abs(s) * eu + eg * eu + \
+            (2.0 ** -8 + (8 + 1.2 * np.abs(g)) * 2.0 ** -23) * np.abs(ref) + 1e-37
+        assert (np.abs(h[rows] - ref) <= tol * 1.02).all()
+        hs = h[rows]
+        out[rows] = hs @ L.w2[e].T
+        tiny = 2.0 ** -38 * np.abs(hs).max(1, keepdims=True)
+        mag[rows] = _acc_bound(w.m) * (np.abs(hs) @ np.abs(L.w2[e]).T) + tiny * np.abs(L.w2[e]).sum(1)
+    y, top = L.combine(out, b, d)
+    err, _ = L.combine(mag, b, d)
+    tol = 2.0 ** -8 * np.abs(y) + np.abs(err) + (w.k + 2) * 2.0 ** -24 * top + 1e-37
+    assert (np.abs(mp.f64(b.y) - y) <= tol * 1.02).all()
+    assert moe.moe_get_device_status(L.ws) == 0
+
+
+FEW_CASES = [
+    dict(T=1, E=1, k=1, m=16, d=32), dict(T=1, E=8, k=2, m=64, d=256),
+    dict(T=3, E=6, k=3, m=172, d=512, noisy=True, router=moe.ST),
+    dict(T=8, E=8, k=2, m=344, d=1024, cap=1), dict(T=9, E=16, k=4, m=100, d=320, noisy=True, bias=True),
+    dict(T=16, E=32, k=8, m=48, d=160, rescale=False), dict(T=16, E=4, k=2, m=40, d=96, cap=0),
+    dict(T=5, E=5, k=1, m=1000, d=64), dict(T=13, E=3, k=3, m=72, d=8192),
+    dict(T=16, E=2, k=2, m=5000, d=64), dict(T=7, E=12, k=5, m=24, d=4096, noisy=True),
+    dict(T=2, E=24, k=8, m=130, d=736, router=moe.ST),
+]
+
+
+@pytest.mark.parametrize("case", FEW_CASES, ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_layer_few(case):
+    L = _Layer(**case)
+    b = moe.Mx4Buffers(L.p, act=moe.MX4_ACT_BF16)
+    for t in (b.y, b.h):
+        t.fill_(float("nan"))
+    L.run(moe.MX4_ACT_BF16, b)
+    _check_few(L, b)
+    y = b.y.clone()
+    L.run(moe.MX4_ACT_BF16, b)  # the same bits again
+    assert torch.equal(b.y.view(torch.int16), y.view(torch.int16))
+
+
+def test_layer_few_nan_token():
+    """A token whose logits are not finite is dropped (y = 0, status set); the others are
+    what they are without it."""
+    L = _Layer(T=4, E=4, k=2, m=64, d=128)
+    good = L.run(moe.MX4_ACT_BF16).y.clone()
+    L.dev["x"][2, 5] = float("inf")
+    L.dev["x"][2, 6] = float("nan")
+    b = L.run(moe.MX4_ACT_BF16)
+    assert moe.moe_get_device_status(L.ws) == moe.MOE_ERR_DEVICE_BADINDEX
+    assert (b.topk_idx[2] == -1).all() and (b.y[2] == 0).all()
+    for t in (0, 1, 3):
+        assert torch.equal(b.y[t], good[t])
+
+
+def test_layer_few_nan_weights():
+    """A NaN scale reaches exactly the outputs whose weights it belongs to."""
+    L = _Layer(T=3, E=2, k=2, m=32, d=128)
+    L.W.W2_s.view(2, -1)[1, 5 * 16] = 255  # expert 1, W2 row 5, block 0
+    b = L.run(moe.MX4_ACT_BF16)
+    nan = torch.isnan(b.y)
+    assert nan[:, 5].all() and nan.sum() == 3
+
+
+@pytest.mark.parametrize("T,E,k,m,d,cap", [(1, 8, 2, 64, 256, -1), (40, 6, 3, 172, 512, 9),
+                                           (300, 8, 2, 96, 160, -1), (33, 64, 8, 48, 128, -1)])
+def test_layer_rows(T, E, k, m, d, cap):
+    """MX4_ACT_MX4 is its steps: route, tables, mx4 dispatch, experts, combine."""
+    L = _Layer(T=T, E=E, k=k, m=m, d=d, cap=cap, noisy=T % 2 == 0)
+    b = L.run(moe.MX4_ACT_MX4)
+    tab = L.check_tables(b)
+    rt = _Routed(b.topk_idx.cpu(), L.inp["x"], E, m, cap)
+    moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, L.W, rt.h_q, rt.h_s, rt.out, rt.ws)
+    R = tab["R"]
+    assert torch.equal(b.out[:R], rt.out[:R])
+    _check_up(rt, L.w1, L.w3, m)
+    _check_down(rt, L.w2, m)
+    y, top = L.combine(mp.f64(b.out)[:R], b, tab)
+    assert (np.abs(mp.f64(b.y) - y) <= 2.0 ** -8 * np.abs(y) + (k + 2) * 2.0 ** -24 * top + 1e-37).all()
+
+
+@pytest.mark.parametrize("act", [moe.MX4_ACT_BF16, moe.MX4_ACT_MX4])
+def test_layer_empty_batch(act):
+    L = _Layer(T=1, E=4, k=2, m=32, d=64)
+    p = moe.params(0, 64, 4, 2, 32, balance_lambda=0.01)
+    b = moe.Mx4Buffers(p, act=None)
+    moe.moe_forward_mx4(p, L.dev["x"][:0], L.dev["Wg"], L.W, L.ws, b, act=act)
+    assert b.counts.tolist() == [0] * 4 and b.offsets.tolist() == [0] * 5 and b.loss.item() == 0
+
+
+@pytest.mark.parametrize("act", [moe.MX4_ACT_BF16, moe.MX4_ACT_MX4])
+def test_layer_graphs_and_streams(act):
+    """Two captured graphs and eager calls that share the workspace, one after the other."""
+    A, B = _Layer(T=5, E=8, k=2, m=96, d=256), _Layer(T=11, E=8, k=2, m=96, d=256)
+    B.ws = A.ws = moe.Workspace(B.p)
+    refs = [L.run(act).y.clone() for L in (A, B)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, bufs = [], []
+    with torch.cuda.stream(s):
+        for L in (A, B):
+            b = moe.Mx4Buffers(L.p, act=act)
+            L.run(act, b)
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                L.run(act, b)
+            graphs.append(g)
+            bufs.append(b)
+        for _ in range(3):
+            for g, b, L, ref in zip(graphs, bufs, (A, B), refs):
+                b.y.fill_(float("nan"))
+                g.replay()
+                assert torch.equal(b.y, ref)
+                assert torch.equal(L.run(act).y, ref)
+    s.synchronize()
+    assert moe.moe_get_device_status(A.ws) == 0

@@ -136,3 +136,54 @@ def test_expert_refusals(L):
                 assert ("'%s'" % names[i]).encode() in L.moe_last_error_string()
             a[i] = _fake(i, 8)
             assert fn(C.byref(p), *a, ws, n, None) == moe.MOE_ERR_ALIGN
+
+
+def test_forward_refusals(L):
+    p = moe.params(16, 64, 8, 2, 16)
+    n = moe.moe_workspace_size(p)
+    ws = _fake(40)
+
+    def call(p=p, act=moe.MX4_ACT_BF16, n=n, drop=(), skew=(), noise=False):
+        b = moe._Mx4Buffers()
+        for i, f in enumerate(moe._MX4_FIELDS):
+            if f in ("Wnoise", "noise") and not noise:
+                continue
+            if f not in drop:
+                setattr(b, f, 0x100000 + 4096 * i + (8 if f in skew else 0))
+        return L.moe_forward_mx4(C.byref(p), C.byref(b), act, ws, n, None)
+
+    assert L.moe_forward_mx4(C.byref(p), None, 0, ws, n, None) == moe.MOE_ERR_INVALID_ARG
+    assert call(act=2) == moe.MOE_ERR_INVALID_ARG
+    assert call(n=n - 1) == moe.MOE_ERR_WORKSPACE
+    big = 1 << 26
+    assert call(moe.params(16, 64, 8, 2, 16, dtype=moe.MOE_F32), n=big) == moe.MOE_ERR_DTYPE
+    assert call(moe.params(16, 72, 8, 2, 16), n=big) == moe.MOE_ERR_SHAPE
+    assert call(moe.params(17, 64, 8, 2, 16), n=big) == moe.MOE_ERR_UNSUPPORTED
+    assert b"16 tokens" in L.moe_last_error_string()
+    assert call(moe.params(4, 64, 33, 2, 16), n=big) == moe.MOE_ERR_UNSUPPORTED
+    assert call(moe.params(4, 64, 17, 2, 16), n=big, noise=True) == moe.MOE_ERR_UNSUPPORTED
+    assert call(noise=True, drop=("noise",)) == moe.MOE_ERR_INVALID_ARG
+    for f in moe._MX4_FIELDS:
+        if f in ("Wnoise", "noise", "bias", "router_packed", "x_q", "x_s", "h_q", "h_s", "out"):
+            continue
+        assert call(drop=(f,)) == moe.MOE_ERR_INVALID_ARG, f
+        assert call(skew=(f,)) == moe.MOE_ERR_ALIGN, f
+    for f in ("x_q", "x_s", "h_q", "h_s", "out"):
+        assert call(act=moe.MX4_ACT_MX4, drop=(f,)) == moe.MOE_ERR_INVALID_ARG, f
+        assert call(act=moe.MX4_ACT_MX4, skew=(f,)) == moe.MOE_ERR_ALIGN, f
+
+
+def test_buffers_given_by_name():
+    import torch
+    p = moe.params(4, 64, 8, 2, 16)
+    y = torch.zeros(4, 64, dtype=torch.bfloat16)
+    b = moe.Mx4Buffers(p, device="cpu", y=y)
+    assert b.y is y and b.out.shape == (8, 64) and b.h.shape == (8, 16)
+    assert moe.Mx4Buffers(p, act=moe.MX4_ACT_BF16, device="cpu").x_q is None
+    assert moe.Mx4Buffers(p, act=moe.MX4_ACT_MX4, device="cpu").h is None
+    with pytest.raises(TypeError):
+        moe.Mx4Buffers(p, device="cpu", nothing=y)
+    with pytest.raises(ValueError):
+        moe.Mx4Buffers(p, device="cpu", y=y[:3])
+    with pytest.raises(ValueError):
+        moe.Mx4Buffers(p, device="cpu", y=y.float())

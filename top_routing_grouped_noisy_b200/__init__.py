@@ -34,6 +34,7 @@ __all__ = [
     "moe_mx4_codes_bytes", "moe_mx4_scales_bytes", "moe_mx4_rows_bytes",
     "moe_mx4_row_scales_bytes", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_dispatch",
     "moe_expert_up_mx4", "moe_expert_down_mx4", "moe_expert_ffn_mx4", "Mx4Experts",
+    "moe_forward_mx4", "Mx4Buffers", "MX4_ACT_BF16", "MX4_ACT_MX4", "MX4_FEW_TOKENS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,6 +60,9 @@ COPY = 1
 STACKED = 2
 EP_CAPACITY_GLOBAL = 0
 EP_CAPACITY_LOCAL = 1
+MX4_ACT_BF16 = 0
+MX4_ACT_MX4 = 1
+MX4_FEW_TOKENS = 16
 
 
 class MoeError(RuntimeError):
@@ -80,6 +84,16 @@ _BUF_FIELDS = ["x", "Wg", "Wnoise", "noise", "bias", "W13_e", "W2_e", "y", "loss
 
 class _Buffers(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in _BUF_FIELDS]
+
+
+_MX4_FIELDS = ["x", "Wg", "Wnoise", "noise", "bias", "W13_q", "W13_s", "W2_q", "W2_s",
+               "router_packed", "y", "loss", "counts", "importance", "f", "P", "topk_idx", "topk_w",
+               "probs_sum", "row_token", "slot_row", "kept", "offsets", "h", "x_q", "x_s", "h_q",
+               "h_s", "out"]
+
+
+class _Mx4Buffers(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in _MX4_FIELDS]
 
 
 _BWD_FIELDS = ["dy", "dx", "dWg", "dWnoise", "dbias", "dW13_e", "dW2_e", "d_out", "dG", "dh",
@@ -165,6 +179,7 @@ def lib():
             "moe_expert_up_mx4": (C.c_int, [P, v, v, v, v, v, v, v, v, sz, v]),
             "moe_expert_down_mx4": (C.c_int, [P, v, v, v, v, v, v, v, sz, v]),
             "moe_expert_ffn_mx4": (C.c_int, [P, v, v, v, v, v, v, v, v, v, v, v, sz, v]),
+            "moe_forward_mx4": (C.c_int, [P, C.POINTER(_Mx4Buffers), i32, v, sz, v]),
             "moe_pipeline_create": (C.c_int, [P, v, v, v, v, v, i32, C.POINTER(v)]),
             "moe_pipeline_submit": (C.c_int, [v, v, v, v, v, C.POINTER(i64)]),
             "moe_pipeline_wait": (C.c_int, [v, i64]),
@@ -824,3 +839,54 @@ def moe_expert_ffn_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, out, ws, s
     _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets), _p(W.W13_q),
                                     _p(W.W13_s), _p(W.W2_q), _p(W.W2_s), _p(h_q), _p(h_s),
                                     _p(out), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+class Mx4Buffers:
+    """Outputs and intermediates of moe_forward_mx4 for layer p, allocated with torch.
+    ``act`` limits the intermediates to those of one form (None: both).  A tensor given by
+    name (Mx4Buffers(p, y=mine)) is used instead of a new one."""
+
+    def __init__(self, p: Params, act=None, device="cuda", **given):
+        T, d, E, k, m = p.T, p.d, p.E, p.k, p.m
+        rows = T * k
+        i32, f32, b16, u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+        shapes = dict(y=((T, d), b16), loss=((1,), f32), counts=((E,), i32),
+                      importance=((E,), f32), f=((E,), f32), P=((E,), f32),
+                      topk_idx=((T, k), i32), topk_w=((T, k), f32), probs_sum=((E,), f32),
+                      row_token=((rows,), i32), slot_row=((T, k), i32), kept=((E,), i32),
+                      offsets=((E + 1,), i32))
+        if act != MX4_ACT_MX4:
+            shapes["h"] = ((max(rows, 1), h_ld(m)), b16)
+        if act != MX4_ACT_BF16:
+            for n, K in (("x", d), ("h", m)):
+                shapes[n + "_q"] = ((moe_mx4_rows_bytes(p, K),), u8)
+                shapes[n + "_s"] = ((moe_mx4_row_scales_bytes(p, K),), u8)
+            shapes["out"] = ((rows, d), b16)
+        bad = set(given) - set(_MX4_FIELDS[10:])
+        if bad:
+            raise TypeError("not a buffer of moe_forward_mx4: %s" % ", ".join(sorted(bad)))
+        for n in _MX4_FIELDS[10:]:
+            t = given.get(n)
+            if t is None and n in shapes:
+                t = torch.empty(shapes[n][0], dtype=shapes[n][1], device=device)
+            elif t is not None and n in shapes:
+                need = 1
+                for v in shapes[n][0]:
+                    need *= v
+                if t.dtype != shapes[n][1] or t.numel() < need:
+                    raise ValueError("%s needs %d elements of %s" % (n, need, shapes[n][1]))
+            setattr(self, n, t)
+
+
+def moe_forward_mx4(p, x, Wg, W: Mx4Experts, ws, bufs: Mx4Buffers, act=MX4_ACT_BF16, Wnoise=None,
+                    noise=None, bias=None, router_packed=None, stream=None):
+    """The whole layer on mx4 expert weights (include/moe.h): at most 16 tokens with bf16
+    activations (MX4_ACT_BF16), or any number with quantised rows (MX4_ACT_MX4)."""
+    b = _Mx4Buffers()
+    vals = dict(x=x, Wg=Wg, Wnoise=Wnoise, noise=noise, bias=bias, W13_q=W.W13_q, W13_s=W.W13_s,
+                W2_q=W.W2_q, W2_s=W.W2_s, router_packed=router_packed)
+    for n in _MX4_FIELDS:
+        setattr(b, n, _p(vals[n] if n in vals else getattr(bufs, n)))
+    _check(lib().moe_forward_mx4(C.byref(p), C.byref(b), int(act), ws.ptr, ws.nbytes,
+                                 _stream(stream)))
+    return bufs

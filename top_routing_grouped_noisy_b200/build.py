@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "partition.cu", "router.cu", "router_tc.cu", "dispatch.cu", "ffn_simt.cu",
            "ffn_tc.cu", "decode.cu", "combine.cu", "pipeline.cu",
            "cluster.cu", "bwd_tc.cu", "bwd.cu", "ep.cu",
-           "mx4_quant.cu", "mx4_gemm.cu", "mx4_api.cu"]
+           "mx4_quant.cu", "mx4_gemm.cu", "mx4_few.cu",
+           "mx4_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
 

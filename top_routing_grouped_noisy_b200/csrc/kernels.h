@@ -199,4 +199,9 @@ cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *h
                             const int32_t *offsets, const void *W2q, const void *W2s, void *out,
                             int32_t *status, cudaStream_t s);
 
+// the whole layer for 1..16 tokens on mx4 weights and bf16 activations (cooperative)
+bool mx4_few_fits(const moe_params_t *p, bool noisy);
+cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, char *ws,
+                           cudaStream_t s);
+
 }  // namespace moe

@@ -43,6 +43,12 @@ int mx_ptr(const char *fn, const void *ptr, const char *name)
             MX_PTR(ptr);                                  \
     } while (0)
 
+#define MX_OPT(ptr)                                       \
+    do {                                                  \
+        if ((ptr) != nullptr)                             \
+            MX_PTR(ptr);                                  \
+    } while (0)
+
 int mx_after(const char *fn, cudaError_t e)
 {
     if (e == cudaSuccess)
@@ -61,7 +67,7 @@ int mx_params(const char *fn, const moe_params_t *p)
     return MOE_OK;
 }
 
-// a bf16 layer and its workspace (`tensor core` calls)
+// a bf16 layer and its workspace
 int mx_layer(const char *fn, const moe_params_t *p, void *ws, size_t ws_bytes)
 {
     const int rc = mx_params(fn, p);
@@ -230,6 +236,78 @@ int moe_expert_ffn_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
                                 stream)) != MOE_OK)
         return rc;
     return moe_expert_down_mx4(p, h_q, h_s, offsets, W2_q, W2_s, out, ws, ws_bytes, stream);
+}
+
+int moe_forward_mx4(const moe_params_t *p, const moe_mx4_buffers_t *b, int32_t act, void *ws,
+                    size_t ws_bytes, void *stream)
+{
+    const char *fn = "moe_forward_mx4";
+    int rc = mx_layer(fn, p, ws, ws_bytes);
+    if (rc != MOE_OK)
+        return rc;
+    if (b == nullptr)
+        return mx_fail(MOE_ERR_INVALID_ARG, fn, "buffers is NULL");
+    if (act != MOE_MX4_ACT_BF16 && act != MOE_MX4_ACT_MX4)
+        return mx_fail(MOE_ERR_INVALID_ARG, fn, "act is neither MOE_MX4_ACT_BF16 nor MOE_MX4_ACT_MX4");
+    MX_TOK(b->x);
+    MX_PTR(b->Wg);
+    MX_OPT(b->Wnoise);
+    MX_OPT(b->noise);
+    MX_OPT(b->bias);
+    MX_OPT(b->router_packed);
+    MX_PTR(b->W13_q);
+    MX_PTR(b->W13_s);
+    MX_PTR(b->W2_q);
+    MX_PTR(b->W2_s);
+    MX_TOK(b->y);
+    MX_PTR(b->loss);
+    MX_PTR(b->counts);
+    MX_PTR(b->importance);
+    MX_PTR(b->f);
+    MX_PTR(b->P);
+    MX_TOK(b->topk_idx);
+    MX_TOK(b->topk_w);
+    MX_PTR(b->probs_sum);
+    MX_TOK(b->row_token);
+    MX_TOK(b->slot_row);
+    MX_PTR(b->kept);
+    MX_PTR(b->offsets);
+    if (b->Wnoise != nullptr && b->noise == nullptr && p->T > 0)
+        return mx_fail(MOE_ERR_INVALID_ARG, fn, "Wnoise given without the noise draws");
+    if (act == MOE_MX4_ACT_BF16 && p->T > 0) {
+        if (p->T > MOE_MX4_FEW_TOKENS)
+            return mx_fail(MOE_ERR_UNSUPPORTED, fn, "MOE_MX4_ACT_BF16 takes at most 16 tokens");
+        if (!mx4_few_fits(p, b->Wnoise != nullptr))
+            return mx_fail(MOE_ERR_UNSUPPORTED, fn,
+                           "MOE_MX4_ACT_BF16 takes at most 32 experts, 16 with noise");
+        MX_PTR(b->h);
+        return mx_after(fn, launch_mx4_few(p, b, static_cast<char *>(ws), (cudaStream_t)stream));
+    }
+    MX_TOK(b->x_q);
+    MX_TOK(b->x_s);
+    MX_TOK(b->h_q);
+    MX_TOK(b->h_s);
+    MX_TOK(b->out);
+    char *w = static_cast<char *>(ws);
+    int32_t *status = reinterpret_cast<int32_t *>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = launch_route(p, b->x, b->Wg, b->Wnoise, b->router_packed, b->noise, b->bias,
+                                 b->topk_idx, b->topk_w, b->probs_sum, b->importance, w, status, s);
+    if (e == cudaSuccess)
+        e = launch_dispatch(p, nullptr, b->topk_idx, nullptr, b->row_token, b->slot_row, b->counts,
+                            b->kept, b->offsets, w, status, true, s);
+    if (e == cudaSuccess && p->T > 0) {
+        if ((e = launch_mx4_dispatch(p, b->x, b->topk_idx, b->slot_row, b->offsets, b->x_q, b->x_s,
+                                     s)) == cudaSuccess &&
+            (e = launch_mx4_up(p, b->x_q, b->x_s, b->offsets, b->W13_q, b->W13_s, b->h_q, b->h_s,
+                               status, s)) == cudaSuccess &&
+            (e = launch_mx4_down(p, b->h_q, b->h_s, b->offsets, b->W2_q, b->W2_s, b->out, status,
+                                 s)) == cudaSuccess)
+            e = launch_combine(p, b->out, b->slot_row, b->topk_w, b->y, s);
+    }
+    if (e == cudaSuccess)
+        e = launch_gate_stats(p, b->counts, b->probs_sum, b->f, b->P, b->loss, s);
+    return mx_after(fn, e);
 }
 
 }  // extern "C"
