@@ -32,6 +32,7 @@
 // Rows are enumerated in the order of the scale tiles (4 rows that lie 32 apart share 16
 // bytes of scales), so that the scale words of an item fill whole sectors.
 #include <mutex>
+#include <type_traits>
 
 #include "gate.cuh"
 #include "mx4.cuh"
@@ -48,11 +49,10 @@ constexpr int kChunkCols = 128;
 constexpr int kChunkBytes = 16 * 64 + 64;     // codes, scale words
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
-constexpr int kMaxDepth = 6;
-constexpr int kMinRegion = 32 * 1024;         // the warps' partial logits
-constexpr int kMaxRegion = 136 * 1024;
-constexpr int kMaxWindow = 4096;              // columns staged at once (a warp's registers)
-constexpr size_t kSmemCap = 212 * 1024;       // dynamic; the static tables take 9 KB
+constexpr int kMaxRegion = 136 * 1024;        // staged activations
+constexpr int kMaxWindow = 8192;              // columns staged at once
+constexpr int kMaxInv = 1088;                 // (row, chunk) scales of a window
+constexpr size_t kSmemCap = 212 * 1024;       // dynamic; the static tables take 12 KB
 
 struct Args {
     const bf16 *x, *Wg, *Wn;
@@ -65,28 +65,26 @@ struct Args {
     uint64_t wait_ns;
     float lambda, scale;
     int T, d, m, E, k, C, router_type;
-    int region, depth, batch, win1, win2;  // bytes; ring chunks; items per reduction; columns
+    int region, red, batch, win1, win2;  // bytes, bytes, items per reduction, columns staged
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+// 16 or 4 bytes to shared memory; zeros where `on` is false (nothing is read then)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src)
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool on)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 4 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest depth - 1 groups have landed
-__device__ __forceinline__ void cp_wait(int depth)
+template <int N> __device__ __forceinline__ void cp_wait()  // all but the newest N groups
 {
-    switch (depth) {
-    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 5: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
@@ -130,7 +128,7 @@ struct UpItems {
     __device__ __forceinline__ UpItems(int nsel, int m)
     {
         per = (m + 63) / 64 * 16;
-        const int64_t all = (int64_t)nsel * per;
+        const uint32_t all = (uint32_t)(nsel * per);  // at most 2^23, times the grid below 2^32
         lo = (int)(blockIdx.x * all / gridDim.x);
         hi = (int)((blockIdx.x + 1) * all / gridDim.x);
         const int n0 = min(hi - lo, per - (per > 0 ? lo % per : 0));
@@ -170,7 +168,7 @@ struct DownItems {
     int lo, hi, per;  // per: items of an expert
     __device__ __forceinline__ explicit DownItems(int d)
     {
-        const int64_t all = (d + 127) / 128 * 32;
+        const uint32_t all = (uint32_t)((d + 127) / 128 * 32);
         lo = (int)(blockIdx.x * all / gridDim.x);
         hi = (int)((blockIdx.x + 1) * all / gridDim.x);
         per = (hi - lo + 3) / 4;
@@ -189,47 +187,47 @@ __device__ __forceinline__ int down_column(int q, int s)
 }
 
 // --------------------------------------------------------------------- one product phase
-// The rows of the weights that A row r (0..15) of item i holds; -1: none.
-struct Rows {
-    const uint8_t *codes, *scales;  // of the item's expert
-    int row;                        // of the expert's matrix, -1 none
-};
+// Items of a phase, at most kItems at a time, as a table in shared memory: expert, quads and
+// first quad packed into a word (the divisions behind them are made once per item, not by
+// every lane that loads or multiplies it).
+constexpr int kItems = 512;
+__device__ __forceinline__ int32_t item_pack(int e, int q, int n) { return e | n << 5 | q << 8; }
+__device__ __forceinline__ int item_expert(int32_t v) { return v & 31; }
+__device__ __forceinline__ int item_quads(int32_t v) { return v >> 5 & 7; }
+__device__ __forceinline__ int item_first(int32_t v) { return v >> 8; }
 
 template <bool UP>
 struct Phase {
     const Args &a;
-    UpItems up;
-    DownItems down;
-    int n_items, K32, tk, win, n_win;
-    const int32_t *sel;
-    __device__ __forceinline__ Phase(const Args &args, int nsel, const int32_t *s_sel)
-        : a(args), up(nsel, args.m), down(args.d), sel(s_sel)
+    const int32_t *items;
+    int n_items;                    // in the table
+    int K32, tk, win, n_win;
+    const uint8_t *codes, *scales;  // of all experts
+    int64_t codes_e, scales_e;      // bytes of an expert's
+    __device__ __forceinline__ Phase(const Args &args, const int32_t *table)
+        : a(args), items(table), n_items(0)
     {
+        const int rows = UP ? 2 * round_up(a.m, 16) : a.d;
         K32 = UP ? a.d : mx4_k32(a.m);
-        n_items = nsel == 0 ? 0 : (UP ? (up.hi > up.lo ? up.count() : 0) : nsel * down.per);
         tk = (K32 + 127) / 128;
         win = UP ? a.win1 : a.win2;
         n_win = (K32 + win - 1) / win;
+        codes = UP ? a.W13q : a.W2q;
+        scales = UP ? a.W13s : a.W2s;
+        codes_e = (int64_t)rows * (K32 / 2);
+        scales_e = (int64_t)((rows + 127) / 128) * tk * kMx4Tile;
     }
-    __device__ __forceinline__ Rows rows(int i, int r) const
+    // the row of the expert's matrix that A row r (0..15) of an item holds; -1: none
+    __device__ __forceinline__ int row(int32_t item, int r) const
     {
-        int is, q, n;
-        Rows o;
+        const int q = item_first(item), n4 = 4 * item_quads(item);
         if constexpr (UP) {
-            up.get(i, is, q, n);
-            const int e = sel[is], m16 = round_up(a.m, 16), s = r & 7;
-            const int nr = up_neuron(q, s);
-            o.codes = a.W13q + (int64_t)e * 2 * m16 * (K32 / 2);
-            o.scales = a.W13s + (int64_t)e * ((2 * m16 + 127) / 128) * tk * kMx4Tile;
-            o.row = (s < 4 * n && nr < a.m) ? (nr / 16) * 32 + nr % 16 + (r >= 8 ? 16 : 0) : -1;
+            const int s = r & 7, nr = up_neuron(q, s);
+            return (s < n4 && nr < a.m) ? (nr >> 4) * 32 + (nr & 15) + (r >= 8 ? 16 : 0) : -1;
         } else {
-            down.get(i, is, q, n);
-            const int e = sel[is], col = down_column(q, r);
-            o.codes = a.W2q + (int64_t)e * a.d * (K32 / 2);
-            o.scales = a.W2s + (int64_t)e * ((a.d + 127) / 128) * tk * kMx4Tile;
-            o.row = (r < 4 * n && col < a.d) ? col : -1;
+            const int col = down_column(q, r);
+            return (r < n4 && col < a.d) ? col : -1;
         }
-        return o;
     }
     // chunks [lo, hi) of window w that warp ks of a group takes
     __device__ __forceinline__ void share(int w, int ks, int &lo, int &hi) const
@@ -241,49 +239,65 @@ struct Phase {
     }
 };
 
-// Loader state of one warp: the chunks of a phase in the order the products take them:
-// batches of items, windows of columns, the group's items, the warp's chunks.
-template <bool UP>
+// Loader state of one warp: the chunks of a phase's table in the order the products take
+// them: batches of items, windows of columns, the group's items, the warp's chunks.
+template <bool UP, int DEPTH>
 struct Loader {
     const Phase<UP> &p;
-    uint32_t ring;       // this warp's stages
-    int depth, stage;
-    int grp, ks, b0, w, i, c, hi;
+    uint32_t ring, st, dst;  // this warp's stages, the next one, this lane's place in it
+    int b0, w, i, c, hi;
     const uint8_t *src0, *src1, *ssrc;  // this lane's 16-byte pieces (two rows), its scale word
-    __device__ __forceinline__ Loader(const Phase<UP> &ph, uint32_t r, int dp, int warp)
-        : p(ph), ring(r), depth(dp), stage(0), grp(warp / KS), ks(warp % KS), b0(0), w(0), i(grp),
-          c(0), hi(0)
+    bool on0, on1, ons;
+    __device__ __forceinline__ Loader(const Phase<UP> &ph, uint32_t r)
+        : p(ph), ring(r), b0(0), w(0)
     {
+        const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
+        dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+        restart();
+    }
+    __device__ __forceinline__ int grp() const { return (int)(threadIdx.x >> 5) / KS; }
+    // from the start of a (refilled) table: the first chunks of the ring
+    __device__ __forceinline__ void restart()
+    {
+        b0 = w = 0;
+        st = ring;
+        i = grp();
         open();
+#pragma unroll 1
+        for (int n = 0; n < DEPTH - 1; ++n)
+            issue();
     }
     // moves to the first item and window from (b0, w, i) on that has a chunk
     __device__ __forceinline__ void open()
     {
         while (b0 < p.n_items) {
             int lo;
-            p.share(w, ks, lo, hi);
+            p.share(w, (int)(threadIdx.x >> 5) % KS, lo, hi);
             if (i < min(b0 + p.a.batch, p.n_items) && lo < hi) {
                 c = lo;
                 const int lane = threadIdx.x & 31;
-                const int half = p.K32 / 2;
-                const Rows r0 = p.rows(i, lane >> 2), r1 = p.rows(i, (lane >> 2) + 8);
-                src0 = r0.row < 0 ? nullptr : r0.codes + (int64_t)r0.row * half + (lane & 3) * 16;
-                src1 = r1.row < 0 ? nullptr : r1.codes + (int64_t)r1.row * half + (lane & 3) * 16;
-                const Rows rs = p.rows(i, lane & 15);
-                ssrc = (lane >= 16 || rs.row < 0)
-                           ? nullptr
-                           : rs.scales + (int64_t)(rs.row / 128) * p.tk * kMx4Tile +
-                                 (rs.row % 32) * 16 + (rs.row % 128) / 32 * 4;
+                const int32_t item = p.items[i];
+                const int e = item_expert(item);
+                const int r0 = p.row(item, lane >> 2), r1 = p.row(item, (lane >> 2) + 8);
+                const int rs = p.row(item, lane & 15);
+                on0 = r0 >= 0;
+                on1 = r1 >= 0;
+                ons = rs >= 0 && lane < 16;
+                const uint8_t *ce = p.codes + e * p.codes_e + (lane & 3) * 16 + lo * 64;
+                src0 = ce + (int64_t)max(r0, 0) * (p.K32 / 2);
+                src1 = ce + (int64_t)max(r1, 0) * (p.K32 / 2);
+                const int q = max(rs, 0);
+                ssrc = p.scales + e * p.scales_e + ((int64_t)(q >> 7) * p.tk + lo) * kMx4Tile +
+                       (q & 31) * 16 + (q >> 5 & 3) * 4;
                 return;
             }
             if (w + 1 < p.n_win) {
                 ++w;
-                i = b0 + grp;
             } else {
                 b0 += p.a.batch;
                 w = 0;
-                i = b0 + grp;
             }
+            i = b0 + grp();
         }
     }
     // issues the next chunk (if any) as one group
@@ -291,175 +305,198 @@ struct Loader {
     {
         if (b0 < p.n_items) {
             const int lane = threadIdx.x & 31;
-            const uint32_t st = ring + (uint32_t)(stage * kChunkBytes);
-            const int row = lane >> 2, piece = lane & 3;
-            // columns past K32 are not loaded: their activations are zero
-            const bool in = c * 64 + piece * 16 < p.K32 / 2;
-            const uint32_t at = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-            if (in && src0 != nullptr)
-                cp16(st + at, src0 + c * 64);
-            if (in && src1 != nullptr)
-                cp16(st + at + 512, src1 + c * 64);
-            if (ssrc != nullptr)
-                cp4(st + 1024 + lane * 4, ssrc + (int64_t)c * kMx4Tile);
-            if (++c == hi) {
+            // columns past K32 are zeros
+            const bool in = c * 64 + (lane & 3) * 16 < p.K32 / 2;
+            cp16(st + dst, src0, in && on0);
+            cp16(st + dst + 512, src1, in && on1);
+            if (lane < 16)
+                cp4(st + 1024 + lane * 4, ssrc, ons);
+            src0 += 64;
+            src1 += 64;
+            ssrc += kMx4Tile;
+            if (__builtin_expect(++c == hi, 0)) {
                 i += NG;
-                if (i >= min(b0 + p.a.batch, p.n_items)) {
-                    if (w + 1 < p.n_win) {
-                        ++w;
-                    } else {
-                        b0 += p.a.batch;
-                        w = 0;
-                    }
-                    i = b0 + grp;
-                }
                 open();
             }
         }
         cp_commit();
-        stage = stage + 1 == depth ? 0 : stage + 1;
+        st = st + kChunkBytes == ring + DEPTH * kChunkBytes ? ring : st + kChunkBytes;
     }
 };
 
-// Stages rows [0, n) (row j from src(j), bf16, columns [c0, c0 + cols) of which those below
-// `valid` exist) as f16 scaled by a power of two, zero up to a whole chunk, and the scales'
-// inverses in inv[j].  One warp per row; called by the whole CTA between two barriers.
-template <class Src>
-__device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, int n, int c0,
-                                           int cols, int valid, Src src)
+// One chunk (128 columns) of one staged row, 16 lanes with 8 bf16 columns each, as f16 scaled
+// by a power of two to a maximum in [2^13, 2^14); returns the scale's inverse.
+__device__ __forceinline__ float scale_chunk(uint4 &v)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nv = (cols + kChunkCols - 1) / kChunkCols * kChunkCols / 8;  // vectors of a row
-    constexpr int V = kMaxWindow / 8 / 32;
-    for (int j = warp; j < n; j += kWarps) {
-        const bf16 *s = src(j);
-        uint4 v[V];
-        uint32_t top = 0;
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            const int col = c0 + (lane + 32 * q) * 8;
-            v[q] = (lane + 32 * q < nv && col < valid)
-                       ? __ldcg(reinterpret_cast<const uint4 *>(s + col))
-                       : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+        top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^(13 - floor(log2(max))): exponent field 127 + 13 - (E - 127), at most 254
+    const uint32_t field = min(267u - (top >> 7), 254u);
+    const float mul = __uint_as_float(field << 23);
+    float f[8];
+    bf16x8_to_f32(v, f);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 hh = __floats2half2_rn(f[2 * i] * mul, f[2 * i + 1] * mul);
+        o[i] = *reinterpret_cast<const uint32_t *>(&hh);
+    }
+    v = make_uint4(o[0], o[1], o[2], o[3]);
+    return mx4_scale(254u - field);
+}
+
+// Stages rows [0, n) of `cols` columns from column c0 (row j at src + j ld, columns below
+// `valid` exist; zeros up to a whole chunk) as scaled f16, inv[j * chunks + ch] the scales'
+// inverses.  With RAW the bf16 rows lie in the region already.  Called by warps
+// [first, 16), each half warp one chunk of one row at a time.
+template <bool RAW>
+__device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, int n, int c0,
+                                           int cols, int valid, const bf16 *src, int64_t ld,
+                                           int first)
+{
+    const int chunks = (cols + kChunkCols - 1) / kChunkCols, total = n * chunks;
+    const int hw = ((int)threadIdx.x >> 4) - 2 * first, l = threadIdx.x & 15;
+    const int step = 2 * (kWarps - first);
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int i0 = hw & ~1; i0 < total; i0 += U * step) {  // both halves of a warp loop alike
+        uint4 v[U];
+        int at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + (hw & 1) + u * step;
+            const int j = i / chunks, col = (i - j * chunks) * kChunkCols + 8 * l;
+            at[u] = i < total ? j * pitch + col * 2 : -1;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (i < total && c0 + col < valid)
+                v[u] = RAW ? *reinterpret_cast<const uint4 *>(region + at[u])
+                           : __ldcg(reinterpret_cast<const uint4 *>(src + j * ld + c0 + col));
+            if (!RAW && c0 + col + 8 > valid) {  // columns past the row's end hold anything
+                uint16_t *e = reinterpret_cast<uint16_t *>(&v[u]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c0 + col + q >= valid)
+                        e[q] = 0;
+            }
         }
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            const int col = c0 + (lane + 32 * q) * 8;
-            if (col < valid && col + 8 > valid) {  // h rows: columns past m hold anything
-                uint16_t *e = reinterpret_cast<uint16_t *>(&v[q]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col + i >= valid)
-                        e[i] = 0;
+        for (int u = 0; u < U; ++u) {
+            const float r = scale_chunk(v[u]);
+            if (at[u] >= 0) {
+                st_v4(region + at[u], v[u]);
+                if (l == 0)
+                    inv[i0 + (hw & 1) + u * step] = r;
             }
-            const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^(13 - floor(log2(max))): exponent field 127 + 13 - (E - 127), at most 254
-        const uint32_t field = min(267u - (top >> 7), 254u);
-        const float mul = __uint_as_float(field << 23);
-        if (lane == 0)
-            inv[j] = mx4_scale(254u - field);
-        char *dst = region + (size_t)j * pitch;
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            if (lane + 32 * q >= nv)
-                break;
-            float fv[8];
-            bf16x8_to_f32(v[q], fv);
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 hh = __floats2half2_rn(fv[2 * i] * mul, fv[2 * i + 1] * mul);
-                o[i] = *reinterpret_cast<const uint32_t *>(&hh);
-            }
-            st_v4(dst + (lane + 32 * q) * 16, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
 
-// acc += A chunk * B: the chunk's 16 rows (stage at `st`) against the token rows at the
-// shared addresses bp[nb] (this lane's B row, its 8 columns of block 0 of the chunk).
-template <int NB>
-__device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, const uint32_t (&bp)[NB],
-                                          int g, int c)
+// 2^s of byte b of a scale word.  The byte moves into the exponent field; 0 becomes 2^-127,
+// and 255 (infinity there) NaN by the multiplication with 0.
+__device__ __forceinline__ float word_scale(uint32_t w, int b)
 {
-    const uint32_t w0 = lds32(st + 1024 + g * 4), w1 = lds32(st + 1024 + (g + 8) * 4);
+    const uint32_t f = (b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7f800000u;
+    const float s = __uint_as_float(max(f, 0x00400000u));
+    return fmaf(s, 0.f, s);
+}
+
+// acc += (A chunk * B) * inv: the chunk's 16 rows (stage at `st`, this lane's words of row g
+// at off[b]) against the token rows at the shared addresses bp[nb] (this lane's B row and 8
+// columns); inv[nb][j]: the scale of the row of token 2c + j.
+template <int NB>
+__device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, const uint32_t (&off)[4],
+                                          const uint32_t (&bp)[NB], const uint32_t (&ip)[NB][2],
+                                          int g)
+{
+    const uint32_t w0 = lds32(st + 1024 + g * 4), w1 = lds32(st + 1056 + g * 4);
+    float sum[NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sum[nb][q] = 0.f;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        const uint32_t at = st + (uint32_t)(g * 64 + ((b ^ ((g >> 1) & 3)) << 4) + c * 4);
         uint32_t a0[4], a1[4];
-        mx4_halves8(lds32(at), a0);
-        mx4_halves8(lds32(at + 512), a1);
-        const float s0 = mx4_scale((w0 >> (8 * b)) & 255u), s1 = mx4_scale((w1 >> (8 * b)) & 255u);
+        mx4_halves8(lds32(st + off[b]), a0);
+        mx4_halves8(lds32(st + off[b] + 512), a1);
+        const float s0 = word_scale(w0, b), s1 = word_scale(w1, b);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const uint4 x = lds128(bp[nb] + b * 64);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(t, a0[0], a1[0], a0[1], a1[1], x.x, x.y);
             mma_f16(t, a0[2], a1[2], a0[3], a1[3], x.z, x.w);
-            acc[nb][0] = fmaf(t[0], s0, acc[nb][0]);
-            acc[nb][1] = fmaf(t[1], s0, acc[nb][1]);
-            acc[nb][2] = fmaf(t[2], s1, acc[nb][2]);
-            acc[nb][3] = fmaf(t[3], s1, acc[nb][3]);
+            sum[nb][0] = fmaf(t[0], s0, sum[nb][0]);
+            sum[nb][1] = fmaf(t[1], s0, sum[nb][1]);
+            sum[nb][2] = fmaf(t[2], s1, sum[nb][2]);
+            sum[nb][3] = fmaf(t[3], s1, sum[nb][3]);
         }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const float i0 = __uint_as_float(lds32(ip[nb][0])), i1 = __uint_as_float(lds32(ip[nb][1]));
+        acc[nb][0] = fmaf(sum[nb][0], i0, acc[nb][0]);
+        acc[nb][1] = fmaf(sum[nb][1], i1, acc[nb][1]);
+        acc[nb][2] = fmaf(sum[nb][2], i0, acc[nb][2]);
+        acc[nb][3] = fmaf(sum[nb][3], i1, acc[nb][3]);
     }
 }
 
 // --------------------------------------------------------------------- the router
-// Logits lg [T][nout] of all tokens: warp w takes 32-column steps [w S / 16, (w + 1) S / 16),
-// staging its rows of [W_g | W_noise] in its own `stage` bytes, as many steps at a time as
-// fit; the warps' sums are added in warp order (`part`).
+// Adds the 32-column steps [s_lo, s_hi) of a window whose bf16 rows lie in the region (step
+// 0 at its start, at global column c0) into acc: the warp's rows of [W_g | W_noise] go to its
+// own `stage` bytes, as many steps at a time as fit.
 template <int NT>
-__device__ void router_logits(const Args &a, char *stage, int stage_bytes, float *part, float *lg)
+__device__ __forceinline__ void router_steps(const Args &a, uint32_t rows, int pitch, int c0,
+                                             int s_lo, int s_hi, char *stage, int stage_bytes,
+                                             float (&acc)[NT][4])
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int E = a.E, T = a.T, d = a.d, nout = a.Wn != nullptr ? 2 * E : E;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int E = a.E, T = a.T, nout = a.Wn != nullptr ? 2 * E : E;
     constexpr int NP = NT * 8;
-    const int steps = d / 32, s_lo = warp * steps / kWarps, s_hi = (warp + 1) * steps / kWarps;
     const int round = stage_bytes / (32 * NP * 2);
     const uint32_t sb = smem_u32(stage);
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            acc[nt][q] = 0.f;
+#pragma unroll 1
     for (int s0 = s_lo; s0 < s_hi; s0 += round) {
         const int n = min(round, s_hi - s0);
+        const int64_t k0 = c0 + s0 * 32;
         __syncwarp();
         if ((E & 7) == 0) {  // rows of whole 16-byte pieces
-            const int pr = nout / 8, total = n * 32 * pr;
+            constexpr int PR = NT;
 #pragma unroll 4
-            for (int i = lane; i < total; i += 32) {
-                const int k = i / pr, o = (i - k * pr) * 8;
-                const bf16 *src = o < E ? a.Wg + (int64_t)(s0 * 32 + k) * E + o
-                                        : a.Wn + (int64_t)(s0 * 32 + k) * E + o - E;
-                st_v4(stage + k * NP * 2 + o * 2, ld_nc(src));
+            for (int i = lane; i < n * 32 * PR; i += 32) {
+                const int k = i / PR, o = (i % PR) * 8;
+                const bf16 *src = o < E ? a.Wg + (k0 + k) * E + o : a.Wn + (k0 + k) * E + o - E;
+                cp16(sb + i * 16, src, true);
             }
+            cp_commit();
+            cp_wait<0>();
         } else {
             const bf16 zero = __float2bfloat16_rn(0.f);
 #pragma unroll 4
             for (int i = lane; i < n * 32 * NP; i += 32) {
-                const int k = i / NP, o = i - k * NP;
-                const int64_t row = (int64_t)(s0 * 32 + k) * E;
+                const int k = i / NP, o = i % NP;
                 reinterpret_cast<bf16 *>(stage)[i] =
-                    o < E ? a.Wg[row + o] : (o < nout ? a.Wn[row + o - E] : zero);
+                    o < E ? a.Wg[(k0 + k) * E + o]
+                          : (o < nout ? a.Wn[(k0 + k) * E + o - E] : zero);
             }
         }
         __syncwarp();
-#pragma unroll 4
+#pragma unroll 2
         for (int s = 0; s < n; ++s) {
-            const bf16 *xs = a.x + (s0 + s) * 32 + 8 * c;
+            // A: 8 consecutive columns of token rows g, g + 8; B of the two products:
+            // columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
+            const uint32_t xa = rows + (uint32_t)(g * pitch + ((s0 + s) * 32 + 8 * c) * 2);
             const uint4 z = make_uint4(0, 0, 0, 0);
-            const uint4 x0 = g < T ? ld_nc(xs + (int64_t)g * d) : z;
-            const uint4 x1 = g + 8 < T ? ld_nc(xs + (int64_t)(g + 8) * d) : z;
-            // B of the two products: columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
+            const uint4 x0 = g < T ? lds128(xa) : z;
+            const uint4 x1 = g + 8 < T ? lds128(xa + 8 * pitch) : z;
             const int i = lane & 7, kk = s * 32 + 8 * (i >> 1) + (i & 1) + 2 * (lane >> 3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -469,6 +506,49 @@ __device__ void router_logits(const Args &a, char *stage, int stage_bytes, float
                 mma_bf16_16816(acc[nt], x0.z, x1.z, x0.w, x1.w, b[2], b[3]);
             }
         }
+    }
+}
+
+// Copies columns [c0, c0 + cols) of x's rows into the region as they are (asynchronous, one
+// group per thread).
+__device__ __forceinline__ void load_x(const Args &a, uint32_t region, int pitch, int c0, int cols)
+{
+    const int nv = cols / 8;
+#pragma unroll 1
+    for (int t = 0; t < a.T; ++t)
+#pragma unroll 2
+        for (int v = threadIdx.x; v < nv; v += kThreads)
+            cp16(region + (uint32_t)(t * pitch + v * 16), a.x + (int64_t)t * a.d + c0 + v * 8, true);
+    cp_commit();
+}
+
+// The logits lg [T][nout] of all tokens: in every window of x, warp w takes the w-th
+// sixteenth of the 32-column steps; the warps' sums are added in warp order.  With one window
+// the region is left holding x.
+template <int NT>
+__device__ __noinline__ void router_logits(const Args &a, char *region, int pitch, char *stage,
+                                           int stage_bytes, float *part, float *lg)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int T = a.T, nout = a.Wn != nullptr ? 2 * a.E : a.E;
+    constexpr int NP = NT * 8;
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            acc[nt][q] = 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < a.d; c0 += a.win1) {
+        const int cols = min(a.win1, a.d - c0), steps = cols / 32;
+        if (c0 > 0) {
+            __syncthreads();  // the last window's rows have been read
+            load_x(a, smem_u32(region), pitch, c0, cols);
+        }
+        cp_wait<0>();
+        __syncthreads();
+        router_steps<NT>(a, smem_u32(region), pitch, c0, warp * steps / kWarps,
+                         (warp + 1) * steps / kWarps, stage, stage_bytes, acc);
     }
     float *pw = part + (size_t)warp * T * NP;
 #pragma unroll
@@ -484,28 +564,27 @@ __device__ void router_logits(const Args &a, char *stage, int stage_bytes, float
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < T * nout; i += kThreads) {
-        const int t = i / nout, o = i - t * nout;
+    if (warp < T && lane < nout) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            sum += part[((size_t)w * T + t) * NP + o];
-        lg[i] = sum;
+            sum += part[((size_t)w * T + warp) * NP + lane];
+        lg[warp * nout + lane] = sum;
     }
-    __syncthreads();
+    __syncwarp();  // the gate of token t is warp t's
 }
 
 // --------------------------------------------------------------------- the kernel
-template <int NB>
+template <int NB, int DEPTH>
 __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_constant__ Args a)
 {
     extern __shared__ __align__(128) char sm[];
     __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE], s_cnt[kMaxE], s_kept[kMaxE];
     __shared__ int32_t s_idx[kMaxRows], s_slot[kMaxRows], s_rtok[kMaxRows];
-    __shared__ float s_w[kMaxRows], s_inv[kMaxRows];
+    __shared__ float s_w[kMaxRows], s_inv[kMaxInv];
     __shared__ float s_lg[MOE_MX4_FEW_TOKENS * 32], s_prob[MOE_MX4_FEW_TOKENS * kMaxE],
         s_gw[MOE_MX4_FEW_TOKENS * kMaxE];
-    __shared__ float s_psum[kMaxE], s_imp[kMaxE];
+    __shared__ int32_t s_items[kItems];
     __shared__ int s_nsel, s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -513,26 +592,27 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     constexpr int RQ = 4 * NB;                      // sums of a lane
     char *region = sm;
     float *red = reinterpret_cast<float *>(sm + a.region);
-    char *ring = sm + a.region + a.batch * KS * 32 * RQ * 4;
-    float *outs = reinterpret_cast<float *>(ring + kWarps * a.depth * kChunkBytes);
-    char *my_ring = ring + warp * a.depth * kChunkBytes;
-    if (threadIdx.x == 0)
-        s_abort = 0;
+    char *ring = sm + a.region + a.red;
+    float *outs = reinterpret_cast<float *>(ring + kWarps * DEPTH * kChunkBytes);
+    char *my_ring = ring + warp * DEPTH * kChunkBytes;
+    const int pitch1 = row_pitch(a.win1), pitch2 = row_pitch(a.win2);
+    const uint32_t region_s = smem_u32(region), ring_s = smem_u32(my_ring);
+    load_x(a, region_s, pitch1, 0, min(a.win1, d));
     // the grid barrier's generation before this launch's barrier (it changes only once
     // every CTA has arrived, this one included)
     int32_t gen = 0;
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        s_abort = 0;
         gen = ld_acquire_gpu(a.gbar + 1);
+    }
 
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
-    float *part = reinterpret_cast<float *>(region);
-    const int sbytes = a.depth * kChunkBytes;
     switch ((nout + 7) / 8) {
-    case 1: router_logits<1>(a, my_ring, sbytes, part, s_lg); break;
-    case 2: router_logits<2>(a, my_ring, sbytes, part, s_lg); break;
-    case 3: router_logits<3>(a, my_ring, sbytes, part, s_lg); break;
-    default: router_logits<4>(a, my_ring, sbytes, part, s_lg); break;
+    case 1: router_logits<1>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
+    case 2: router_logits<2>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
+    case 3: router_logits<3>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
+    default: router_logits<4>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
     }
     if (warp < T)
         gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
@@ -540,63 +620,68 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                         s_idx + warp * k, s_w + warp * k, s_prob + warp * E, s_gw + warp * E,
                         a.status);
     __syncthreads();
-    // ---- dispatch tables: stable by token, assignments past the capacity dropped
-    if (threadIdx.x < E) {
-        const int e = threadIdx.x;
+    // ---- dispatch tables by warp 0 (lane e: expert e): stable by token, assignments past the
+    // capacity dropped; the other warps turn the staged x into scaled f16
+    const bool one_window = d <= a.win1;
+    if (warp == 0) {
         int cnt = 0;
-        float sp = 0.f, sg = 0.f;
         for (int i = 0; i < T * k; ++i)
-            cnt += s_idx[i] == e;
-        for (int t = 0; t < T; ++t) {
-            sp += s_prob[t * E + e];
-            sg += s_gw[t * E + e];
+            cnt += s_idx[i] == lane;
+        cnt = lane < E ? cnt : 0;
+        const int kept = a.C < 0 ? cnt : min(cnt, a.C);
+        int off = kept;  // inclusive prefix sum
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, off, o);
+            off += lane >= o ? v : 0;
         }
-        s_cnt[e] = cnt;
-        s_kept[e] = a.C < 0 ? cnt : min(cnt, a.C);
-        s_psum[e] = sp;
-        s_imp[e] = sg;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int acc = 0, ns = 0;
-        for (int e = 0; e < E; ++e) {
-            s_off[e] = acc;
-            acc += s_kept[e];
-            if (s_kept[e] > 0)
-                s_sel[ns++] = e;
+        const uint32_t used = __ballot_sync(0xffffffffu, kept > 0);
+        if (lane < E) {
+            s_cnt[lane] = cnt;
+            s_kept[lane] = kept;
+            s_off[lane + 1] = off;
+            if (kept > 0)
+                s_sel[__popc(used & ((1u << lane) - 1))] = lane;
         }
-        s_off[E] = acc;
-        s_nsel = ns;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < T * k; i += kThreads) {
-        const int t = i / k, e = s_idx[i];
-        int row = -1;
-        if (e >= 0 && e < E) {
-            int rank = 0;  // the expert's assignments of earlier tokens
-            for (int j = 0; j < t * k; ++j)
-                rank += s_idx[j] == e;
-            if (rank < s_kept[e]) {
-                row = s_off[e] + rank;
-                s_rtok[row] = t;
-            }
+        if (lane == 0) {
+            s_off[0] = 0;
+            s_nsel = __popc(used);
         }
-        s_slot[i] = row;
+        int row = off - kept, left = kept;
+        for (int i = lane; i < T * k; i += 32)
+            s_slot[i] = -1;
+        __syncwarp();
+        for (int t = 0; t < T; ++t)
+            for (int j = 0; j < k; ++j)  // a token names an expert once
+                if (s_idx[t * k + j] == lane && left > 0) {
+                    s_slot[t * k + j] = row;
+                    s_rtok[row] = t;
+                    ++row;
+                    --left;
+                }
+    } else if (one_window) {
+        stage_rows<true>(region, pitch1, s_inv, T, 0, d, d, nullptr, 0, 1);
     }
     __syncthreads();
     const int nsel = s_nsel, R = s_off[E], m8 = round_up(m, 8);
+    uint32_t a_off[4];  // this lane's words of A row g in a chunk
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        a_off[b] = (uint32_t)(g * 64 + ((b ^ ((g >> 1) & 3)) << 4) + c * 4);
 
-    // ---- one product phase: every item's sums, handed to done(item, sum) where
-    // sum(L, q) is value q of lane L
-    auto products = [&](auto &ph, auto &ld, int pitch, auto stage, auto brow, auto done) {
+    // ---- one product phase over the table's items: their sums, handed to done(item, slot,
+    // sum) in the order of a thread's slots (PER threads per item), where sum(L, q) is value
+    // q of lane L
+    auto products = [&](auto &ph, auto &ld, auto per, int pitch, bool staged, auto stage, auto brow,
+                        auto done) {
+        constexpr int PER = decltype(per)::value;
         const int grp = warp / KS, ks = warp % KS;
-        int st = 0;
-        bool staged = false;
+        uint32_t st = ring_s;
         for (int b0 = 0; b0 < ph.n_items; b0 += a.batch) {
             const int b1 = min(b0 + a.batch, ph.n_items);
             for (int w = 0; w < ph.n_win; ++w) {
                 if (!staged || ph.n_win > 1) {
-                    if (staged)
+                    if (b0 + w > 0)
                         __syncthreads();  // the last window's products are done
                     stage(w);
                     __syncthreads();
@@ -605,187 +690,216 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 int lo, hi;
                 ph.share(w, ks, lo, hi);
                 const int c0 = w * (ph.win / kChunkCols);
+                const int chunks = min(ph.win / kChunkCols, ph.tk - c0);
                 for (int i = b0 + grp; i < b1; i += NG) {
-                    uint32_t bp0[NB];
-                    int brw[NB][2];
-                    brow(i, bp0, brw);
+                    uint32_t bp[NB], ip[NB][2];
+                    const int32_t item = ph.items[i];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        bp[nb] = region_s + (uint32_t)(brow(item, nb * 8 + g) * pitch +
+                                                       (lo - c0) * kChunkCols * 2 + 16 * c);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            ip[nb][j] = smem_u32(s_inv + brow(item, nb * 8 + 2 * c + j) * chunks +
+                                                 lo - c0);
+                    }
                     float acc[NB][4];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             acc[nb][q] = 0.f;
+#pragma unroll 1
                     for (int ch = lo; ch < hi; ++ch) {
                         __syncwarp();  // the stage the loader fills next has been read
                         ld.issue();
-                        cp_wait(a.depth);
+                        cp_wait<DEPTH - 1>();
                         __syncwarp();
-                        uint32_t bp[NB];
+                        chunk_mma<NB>(acc, st, a_off, bp, ip, g);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            bp[nb] = bp0[nb] + (uint32_t)((ch - c0) * kChunkCols * 2 + 16 * c);
-                        chunk_mma<NB>(acc, smem_u32(my_ring) + (uint32_t)(st * kChunkBytes), bp, g, c);
-                        st = st + 1 == a.depth ? 0 : st + 1;
+                        for (int nb = 0; nb < NB; ++nb) {
+                            bp[nb] += kChunkCols * 2;
+                            ip[nb][0] += 4;
+                            ip[nb][1] += 4;
+                        }
+                        st = st + kChunkBytes == ring_s + DEPTH * kChunkBytes ? ring_s
+                                                                              : st + kChunkBytes;
                     }
                     float *rw = red + ((size_t)((i - b0) * KS + ks) * 32 + lane) * RQ;
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float v = acc[nb][q] * s_inv[brw[nb][q & 1]];
-                            rw[nb * 4 + q] = w == 0 ? v : rw[nb * 4 + q] + v;
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            rw[nb * 4 + q] = w == 0 ? acc[nb][q] : rw[nb * 4 + q] + acc[nb][q];
                 }
             }
             __syncthreads();
-            for (int i = b0; i < b1; ++i)
-                done(i, [&](int L, int q) {
-                    float s = 0.f;
+            for (int j = threadIdx.x; j < (b1 - b0) * PER; j += kThreads) {
+                const int i = j / PER;
+                done(ph.items[b0 + i], j % PER, [&](int L, int q) {
+                    float v = 0.f;
 #pragma unroll
-                    for (int j = 0; j < KS; ++j)
-                        s += red[((size_t)((i - b0) * KS + j) * 32 + L) * RQ + q];
-                    return s;
+                    for (int u = 0; u < KS; ++u)
+                        v += red[((size_t)(i * KS + u) * 32 + L) * RQ + q];
+                    return v;
                 });
+            }
             if (b1 < ph.n_items)
                 __syncthreads();  // the sums are read before the next batch's are written
         }
     };
 
     // ---- GEMM 1
-    const int pitch1 = row_pitch(a.win1), pitch2 = row_pitch(a.win2);
-    const uint32_t region_s = smem_u32(region);
-    {
-        const Phase<true> ph(a, nsel, s_sel);
-        Loader<true> ld(ph, smem_u32(my_ring), a.depth, warp);
-        for (int i = 0; i < a.depth - 1; ++i)
-            ld.issue();
+    const UpItems up(nsel, m);
+    const int n_up = up.hi > up.lo ? up.count() : 0;
+#pragma unroll 1
+    for (int base = 0; base < n_up; base += kItems) {
+        Phase<true> ph(a, s_items);
+        ph.n_items = min(kItems, n_up - base);
+        if (base > 0)
+            __syncthreads();  // the table's last use is over
+        if ((int)threadIdx.x < ph.n_items) {
+            int is, q, n;
+            up.get(base + threadIdx.x, is, q, n);
+            s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
+        }
+        __syncthreads();
+        Loader<true, DEPTH> ld(ph, ring_s);
         products(
-            ph, ld, pitch1,
+            ph, ld, std::integral_constant<int, 64 * NB>(), pitch1, one_window,
             [&](int w) {
-                stage_rows(region, pitch1, s_inv, T, w * a.win1, min(a.win1, d - w * a.win1), d,
-                           [&](int j) { return a.x + (int64_t)j * d; });
+                stage_rows<false>(region, pitch1, s_inv, T, w * a.win1,
+                                  min(a.win1, d - w * a.win1), d, a.x, d, 0);
             },
-            [&](int i, uint32_t (&bp)[NB], int (&br)[NB][2]) {
-                int is, q, n;
-                ph.up.get(i, is, q, n);
-                const int e = s_sel[is], r0 = s_off[e], nr = s_off[e + 1] - r0;
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    bp[nb] = region_s + (uint32_t)(s_rtok[r0 + min(nb * 8 + g, nr - 1)] * pitch1);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        br[nb][j] = s_rtok[r0 + min(nb * 8 + 2 * c + j, nr - 1)];
-                }
+            [&](int32_t item, int tok) {
+                const int e = item_expert(item), r0 = s_off[e];
+                return s_rtok[min(r0 + tok, s_off[e + 1] - 1)];
             },
-            [&](int i, auto sum) {
-                int is, q, n;
-                ph.up.get(i, is, q, n);
-                const int e = s_sel[is], r0 = s_off[e], nr = s_off[e + 1] - r0;
-                if (threadIdx.x < 64 * NB) {
-                    const int s = threadIdx.x & 7, tok = threadIdx.x >> 3;
-                    const int nrn = up_neuron(q, s), L = s * 4 + (tok & 7) / 2, at = tok / 8 * 4 + (tok & 1);
-                    if (s < 4 * n && nrn < m && tok < nr) {
-                        const float gv = sum(L, at), uv = sum(L, at + 2);
-                        // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
-                        a.h[(int64_t)(r0 + tok) * m8 + nrn] =
-                            __float2bfloat16_rn(__fdividef(gv, 1.0f + __expf(-gv)) * uv);
-                    }
+            [&](int32_t item, int slot, auto sum) {
+                const int e = item_expert(item), r0 = s_off[e], nr = s_off[e + 1] - r0;
+                const int s = slot & 7, tok = slot >> 3;
+                const int nrn = up_neuron(item_first(item), s);
+                const int L = s * 4 + (tok & 7) / 2, at = tok / 8 * 4 + (tok & 1);
+                if (s < 4 * item_quads(item) && nrn < m && tok < nr) {
+                    const float gv = sum(L, at), uv = sum(L, at + 2);
+                    // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
+                    a.h[(int64_t)(r0 + tok) * m8 + nrn] =
+                        __float2bfloat16_rn(__fdividef(gv, 1.0f + __expf(-gv)) * uv);
                 }
             });
     }
 
     // ---- h of every CTA complete: a grid barrier; GEMM 2's first weights travel meanwhile,
     // and CTA 0 writes the routing, the tables and the statistics
-    const Phase<false> ph(a, nsel, s_sel);
-    __syncwarp();
-    Loader<false> ld(ph, smem_u32(my_ring), a.depth, warp);
-    for (int i = 0; i < a.depth - 1; ++i)
-        ld.issue();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const int G = (int)gridDim.x;
+    const DownItems down(d);
+    const int n_down = nsel * down.per;
+    Phase<false> ph(a, s_items);
+    auto fill_down = [&](int base) {
+        ph.n_items = min(kItems, n_down - base);
+        if ((int)threadIdx.x < ph.n_items) {
+            int is, q, n;
+            down.get(base + threadIdx.x, is, q, n);
+            s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
+        }
+    };
+    __syncthreads();  // h of this CTA is written, the table's last use is over
+    if (threadIdx.x == kThreads - 1) {
         __threadfence();  // this CTA's h, ordered before by the barrier above
-        if (atomicAdd(a.gbar, 1) == G - 1) {  // the last to arrive releases the others
+        if (atomicAdd(a.gbar, 1) == (int)gridDim.x - 1) {  // the last to arrive releases all
+            __threadfence();
+            asm volatile("red.relaxed.gpu.global.and.b32 [%0], 0;" ::"l"(a.gbar) : "memory");
             __threadfence();
             atomicAdd(a.gbar + 1, 1);
-            asm volatile("red.relaxed.gpu.global.and.b32 [%0], 0;" ::"l"(a.gbar) : "memory");
-        } else {
-            const uint64_t t0 = globaltimer_ns();
-            while (ld_acquire_gpu(a.gbar + 1) == gen) {
-                if (globaltimer_ns() - t0 > a.wait_ns) {
-                    set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-                    s_abort = 1;
-                    break;
-                }
-                __nanosleep(32);
+        }
+    }
+    fill_down(0);
+    __syncthreads();
+    Loader<false, DEPTH> ld(ph, ring_s);
+    if (threadIdx.x == 0) {
+        const uint64_t t0 = globaltimer_ns();
+        while (ld_acquire_gpu(a.gbar + 1) == gen) {
+            if (globaltimer_ns() - t0 > a.wait_ns) {
+                set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                s_abort = 1;
+                break;
             }
         }
-    } else if (blockIdx.x == 0) {
-        const int nt = kThreads - 32, t1 = (int)threadIdx.x - 32;
-        if (t1 >= 0) {
-            for (int i = t1; i < T * k; i += nt) {
-                a.idx[i] = s_idx[i];
-                a.w[i] = s_w[i];
-                a.slot_row[i] = s_slot[i];
+    } else if (blockIdx.x == 0 && threadIdx.x >= 32) {
+        constexpr int nt = kThreads - 32;
+        const int t1 = (int)threadIdx.x - 32;
+        if (t1 < T * k) {
+            a.idx[t1] = s_idx[t1];
+            a.w[t1] = s_w[t1];
+            a.slot_row[t1] = s_slot[t1];
+        }
+        if (t1 < R)
+            a.row_token[t1] = s_rtok[t1];
+        if (t1 <= E)
+            a.offsets[t1] = s_off[t1];
+        // the gate statistics, in gate_stats_kernel's arithmetic
+        if (t1 < E) {
+            float sp = 0.f, sg = 0.f;
+            for (int t = 0; t < T; ++t) {
+                sp += s_prob[t * E + t1];
+                sg += s_gw[t * E + t1];
             }
-            for (int r = t1; r < R; r += nt)
-                a.row_token[r] = s_rtok[r];
-            for (int e = t1; e <= E; e += nt)
-                a.offsets[e] = s_off[e];
-            // the gate statistics, in gate_stats_kernel's arithmetic
-            for (int e = t1; e < E; e += nt) {
-                a.counts[e] = s_cnt[e];
-                a.kept[e] = s_kept[e];
-                a.probs_sum[e] = s_psum[e];
-                a.importance[e] = s_imp[e];
-                a.f[e] = (float)((double)s_cnt[e] / ((double)T * k));
-                a.P[e] = (float)((double)s_psum[e] / (double)T);
+            a.counts[t1] = s_cnt[t1];
+            a.kept[t1] = s_kept[t1];
+            a.probs_sum[t1] = sp;
+            a.importance[t1] = sg;
+            a.f[t1] = (float)((double)s_cnt[t1] / ((double)T * k));
+            a.P[t1] = (float)((double)sp / (double)T);
+        }
+        if (t1 == nt - 1) {
+            double sfp = 0.0;
+            for (int e = 0; e < E; ++e) {
+                float sp = 0.f;
+                for (int t = 0; t < T; ++t)
+                    sp += s_prob[t * E + e];
+                sfp += ((double)s_cnt[e] / ((double)T * k)) * ((double)sp / (double)T);
             }
-            if (t1 == nt - 1) {
-                double sfp = 0.0;
-                for (int e = 0; e < E; ++e)
-                    sfp += ((double)s_cnt[e] / ((double)T * k)) * ((double)s_psum[e] / (double)T);
-                a.loss[0] = (float)(a.lambda * sfp);
-            }
+            a.loss[0] = (float)(a.lambda * sfp);
         }
     }
     __syncthreads();
 
     // ---- GEMM 2 and the combine of this CTA's columns
     if (!s_abort) {
-        const int ncol = 4 * (ph.down.hi - ph.down.lo);
-        products(
-            ph, ld, pitch2,
-            [&](int w) {
-                const int K = mx4_k32(m);
-                stage_rows(region, pitch2, s_inv, R, w * a.win2, min(a.win2, K - w * a.win2), m,
-                           [&](int j) { return a.h + (int64_t)j * m8; });
-            },
-            [&](int i, uint32_t (&bp)[NB], int (&br)[NB][2]) {
-                const int e = s_sel[i / ph.down.per], r0 = s_off[e], nr = s_off[e + 1] - r0;
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    bp[nb] = region_s + (uint32_t)((r0 + min(nb * 8 + g, nr - 1)) * pitch2);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        br[nb][j] = r0 + min(nb * 8 + 2 * c + j, nr - 1);
-                }
-            },
-            [&](int i, auto sum) {
-                int is, q, n;
-                ph.down.get(i, is, q, n);
-                const int e = s_sel[is], r0 = s_off[e], nr = s_off[e + 1] - r0;
-                if (threadIdx.x < 128 * NB) {
-                    const int s = threadIdx.x & 15, tok = threadIdx.x >> 4;
-                    const int L = (s & 7) * 4 + (tok & 7) / 2, at = tok / 8 * 4 + (tok & 1) + (s & 8) / 4;
-                    if (s < 4 * n && tok < nr)
-                        outs[(size_t)(r0 + tok) * ncol + 4 * (q - ph.down.lo) + s] = sum(L, at);
-                }
-            });
+        const int ncol = 4 * (down.hi - down.lo);
+#pragma unroll 1
+        for (int base = 0; base < n_down;) {
+            products(
+                ph, ld, std::integral_constant<int, 128 * NB>(), pitch2, base > 0,
+                [&](int w) {
+                    const int K = mx4_k32(m);
+                    stage_rows<false>(region, pitch2, s_inv, R, w * a.win2,
+                                      min(a.win2, K - w * a.win2), m, a.h, m8, 0);
+                },
+                [&](int32_t item, int tok) {
+                    const int e = item_expert(item);
+                    return min(s_off[e] + tok, s_off[e + 1] - 1);
+                },
+                [&](int32_t item, int slot, auto sum) {
+                    const int e = item_expert(item), r0 = s_off[e], nr = s_off[e + 1] - r0;
+                    const int s = slot & 15, tok = slot >> 4;
+                    const int L = (s & 7) * 4 + (tok & 7) / 2;
+                    const int at = tok / 8 * 4 + (tok & 1) + (s & 8) / 4;
+                    if (s < 4 * item_quads(item) && tok < nr)
+                        outs[(size_t)(r0 + tok) * ncol + 4 * (item_first(item) - down.lo) + s] =
+                            sum(L, at);
+                });
+            base += kItems;
+            if (base < n_down) {
+                __syncthreads();
+                fill_down(base);
+                __syncthreads();
+                ld.restart();
+            }
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < T * ncol; i += kThreads) {
             const int t = i / ncol, o = i - t * ncol;
-            const int col = down_column(ph.down.lo, o);
+            const int col = down_column(down.lo, o);
             if (col >= d)
                 continue;
             float acc = 0.f;
@@ -797,10 +911,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             a.y[(int64_t)t * d + col] = __float2bfloat16_rn(acc * a.scale);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    cp_wait<0>();
 }
 
 // --------------------------------------------------------------------- host side
+
+constexpr int kDepths = 3;
+constexpr int kDepth[kDepths] = {6, 4, 2};  // chunks of a warp's ring
+typedef void (*Kernel)(const Args);
+static const Kernel kKernel[2][kDepths] = {
+    {mx4_few_kernel<1, 6>, mx4_few_kernel<1, 4>, mx4_few_kernel<1, 2>},
+    {mx4_few_kernel<2, 6>, mx4_few_kernel<2, 4>, mx4_few_kernel<2, 2>}};
 
 static cudaError_t grid_size(int *out)
 {
@@ -815,12 +936,13 @@ static cudaError_t grid_size(int *out)
     std::lock_guard<std::mutex> lk(mu);
     if (sms[dev] == 0) {
         int n = 0;
-        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(mx4_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)kSmemCap)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(mx4_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)kSmemCap)) != cudaSuccess)
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return e;
+        for (int i = 0; i < 2 * kDepths; ++i)
+            if ((e = cudaFuncSetAttribute(kKernel[i / kDepths][i % kDepths],
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)kSmemCap)) != cudaSuccess)
+                return e;
         sms[dev] = n;
     }
     *out = sms[dev];
@@ -828,11 +950,13 @@ static cudaError_t grid_size(int *out)
 }
 
 // Columns staged at once for `rows` activation rows of K columns: all of them if they fit
-// the region and a warp's registers, else as many whole chunks as do.
+// the region and the table of scales, else as many whole chunks as do.
 static int window(int rows, int K)
 {
     const int k128 = (K + kChunkCols - 1) / kChunkCols * kChunkCols;
     int w = (kMaxRegion / rows - 64) / 2 / kChunkCols * kChunkCols;
+    const int t = kMaxInv / rows * kChunkCols;
+    w = w < t ? w : t;
     w = w < kMaxWindow ? w : kMaxWindow;
     return w < k128 ? w : k128;
 }
@@ -893,18 +1017,20 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.win2 = window(R, p->m);
     const int x_bytes = p->T * row_pitch(a.win1), h_bytes = R * row_pitch(a.win2);
     a.region = round_up(x_bytes > h_bytes ? x_bytes : h_bytes, 128);
-    a.region = a.region > kMinRegion ? a.region : kMinRegion;
+    // 16 KB of partial sums a batch; the router's partial logits come there first
     a.batch = nb == 1 ? 8 : 4;
-    const size_t red = (size_t)a.batch * KS * 32 * 4 * nb * 4;
+    const int part = kWarps * p->T * round_up((b->Wnoise != nullptr ? 2 : 1) * p->E, 8) * 4;
+    a.red = a.batch * KS * 32 * 4 * nb * 4;
+    a.red = round_up(a.red > part ? a.red : part, 128);
     const int64_t quads = (p->d + 127) / 128 * 32;
     const size_t outs = (size_t)R * 4 * ((quads + grid - 1) / grid + 1) * 4;
-    const size_t fixed = a.region + red + outs;
-    const size_t per = (size_t)kWarps * kChunkBytes;
-    if (fixed + 2 * per > kSmemCap)
+    const size_t fixed = (size_t)a.region + a.red + outs, per = (size_t)kWarps * kChunkBytes;
+    int di = 0;
+    while (di < kDepths && fixed + kDepth[di] * per > kSmemCap)
+        ++di;
+    if (di == kDepths)
         return cudaErrorInvalidValue;
-    a.depth = (int)((kSmemCap - fixed) / per);
-    a.depth = a.depth < kMaxDepth ? a.depth : kMaxDepth;
-    const size_t smem = fixed + a.depth * per;
+    const size_t smem = fixed + kDepth[di] * per;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -916,8 +1042,7 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launch();
-    e = nb == 1 ? cudaLaunchKernelEx(&cfg, mx4_few_kernel<1>, a)
-                : cudaLaunchKernelEx(&cfg, mx4_few_kernel<2>, a);
+    e = cudaLaunchKernelEx(&cfg, kKernel[nb - 1][di], a);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
