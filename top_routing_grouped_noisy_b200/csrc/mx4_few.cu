@@ -44,9 +44,13 @@ namespace few {
 using tc::smem_u32;
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int KS = 4, NG = kWarps / KS;       // warps that split K, groups of items
 constexpr int kChunkCols = 128;
 constexpr int kChunkBytes = 16 * 64 + 64;     // codes, scale words
+// chunks of a ring stage: two halve the loop's overhead per weight; with two groups of 8
+// tokens the staged activations leave room for single chunks only
+__host__ __device__ constexpr int stage_chunks(int nb) { return nb == 1 ? 2 : 1; }
+__host__ __device__ constexpr int stage_cols(int nb) { return stage_chunks(nb) * kChunkCols; }
+__host__ __device__ constexpr int stage_bytes(int nb) { return stage_chunks(nb) * kChunkBytes; }
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
 constexpr int kMaxRegion = 136 * 1024;        // staged activations
@@ -65,7 +69,7 @@ struct Args {
     uint64_t wait_ns;
     float lambda, scale;
     int T, d, m, E, k, C, router_type;
-    int region, red, batch, win1, win2;  // bytes, bytes, items per reduction, columns staged
+    int region, red, win1, win2;  // bytes, bytes, columns staged
 };
 
 // 16 or 4 bytes to shared memory; zeros where `on` is false (nothing is read then)
@@ -196,16 +200,17 @@ __device__ __forceinline__ int item_expert(int32_t v) { return v & 31; }
 __device__ __forceinline__ int item_quads(int32_t v) { return v >> 5 & 7; }
 __device__ __forceinline__ int item_first(int32_t v) { return v >> 8; }
 
-template <bool UP>
+template <bool UP, int NB>
 struct Phase {
     const Args &a;
     const int32_t *items;
     int n_items;                    // in the table
+    int kshift;                     // 2^kshift warps (a group) split the columns of an item
     int K32, tk, win, n_win;
     const uint8_t *codes, *scales;  // of all experts
     int64_t codes_e, scales_e;      // bytes of an expert's
     __device__ __forceinline__ Phase(const Args &args, const int32_t *table)
-        : a(args), items(table), n_items(0)
+        : a(args), items(table), n_items(0), kshift(0)
     {
         const int rows = UP ? 2 * round_up(a.m, 16) : a.d;
         K32 = UP ? a.d : mx4_k32(a.m);
@@ -216,6 +221,24 @@ struct Phase {
         scales = UP ? a.W13s : a.W2s;
         codes_e = (int64_t)rows * (K32 / 2);
         scales_e = (int64_t)((rows + 127) / 128) * tk * kMx4Tile;
+    }
+    // For n items in the table: the split with the fewest stages on the busiest warp (the
+    // items go round the 16 / 2^kshift groups), the sum of an item's parts counted as half a
+    // stage.
+    __device__ __forceinline__ void set(int n)
+    {
+        n_items = n;
+        const int steps = n_win * ((min(win, K32) + stage_cols(NB) - 1) / stage_cols(NB));
+        int best = 1 << 30;
+#pragma unroll
+        for (int k = 0; k <= 4; ++k) {
+            const int cost = ((n + (kWarps >> k) - 1) >> (4 - k)) *
+                             (2 * ((steps + (1 << k) - 1) >> k) + (k > 0 ? 1 : 0));
+            if (cost < best) {
+                best = cost;
+                kshift = k;
+            }
+        }
     }
     // the row of the expert's matrix that A row r (0..15) of an item holds; -1: none
     __device__ __forceinline__ int row(int32_t item, int r) const
@@ -229,52 +252,61 @@ struct Phase {
             return (r < n4 && col < a.d) ? col : -1;
         }
     }
-    // chunks [lo, hi) of window w that warp ks of a group takes
-    __device__ __forceinline__ void share(int w, int ks, int &lo, int &hi) const
+    // stages [lo, hi) of window w (counted inside it) that this warp takes
+    __device__ __forceinline__ void share(int w, int &lo, int &hi) const
     {
-        const int c0 = w * (win / kChunkCols);
-        const int n = min(win / kChunkCols, tk - c0);
-        lo = c0 + ks * n / KS;
-        hi = c0 + (ks + 1) * n / KS;
+        const int n = (min(win, K32 - w * win) + stage_cols(NB) - 1) / stage_cols(NB);
+        const int ks = (int)(threadIdx.x >> 5) & ((1 << kshift) - 1);
+        lo = (ks * n) >> kshift;
+        hi = ((ks + 1) * n) >> kshift;
     }
+    // chunks staged of window w: whole stages
+    __device__ __forceinline__ int chunks(int w) const
+    {
+        return (min(win, K32 - w * win) + stage_cols(NB) - 1) / stage_cols(NB) * stage_chunks(NB);
+    }
+    __device__ __forceinline__ int group() const { return (int)(threadIdx.x >> 5) >> kshift; }
+    __device__ __forceinline__ int groups() const { return kWarps >> kshift; }
 };
 
-// Loader state of one warp: the chunks of a phase's table in the order the products take
-// them: batches of items, windows of columns, the group's items, the warp's chunks.
-template <bool UP, int DEPTH>
+// Loader state of one warp: the stages of a phase's table in the order the products take
+// them: the group's items, windows of columns, the warp's stages.
+template <bool UP, int NB, int DEPTH>
 struct Loader {
-    const Phase<UP> &p;
+    static constexpr int SB = stage_bytes(NB), SC = stage_chunks(NB);
+    const Phase<UP, NB> &p;
     uint32_t ring, st, dst;  // this warp's stages, the next one, this lane's place in it
-    int b0, w, i, c, hi;
+    int w, i, c, hi;         // c: first chunk of the next stage; hi: end of the warp's share
     const uint8_t *src0, *src1, *ssrc;  // this lane's 16-byte pieces (two rows), its scale word
     bool on0, on1, ons;
-    __device__ __forceinline__ Loader(const Phase<UP> &ph, uint32_t r)
-        : p(ph), ring(r), b0(0), w(0)
+    __device__ __forceinline__ Loader(const Phase<UP, NB> &ph, uint32_t r)
+        : p(ph), ring(r), w(0)
     {
         const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
         dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
         restart();
     }
-    __device__ __forceinline__ int grp() const { return (int)(threadIdx.x >> 5) / KS; }
-    // from the start of a (refilled) table: the first chunks of the ring
+    // from the start of a (refilled) table: the first stages of the ring
     __device__ __forceinline__ void restart()
     {
-        b0 = w = 0;
+        w = 0;
         st = ring;
-        i = grp();
+        i = p.group();
         open();
 #pragma unroll 1
         for (int n = 0; n < DEPTH - 1; ++n)
             issue();
     }
-    // moves to the first item and window from (b0, w, i) on that has a chunk
+    // moves to the first item and window from (i, w) on that has a stage
     __device__ __forceinline__ void open()
     {
-        while (b0 < p.n_items) {
+        while (i < p.n_items) {
             int lo;
-            p.share(w, (int)(threadIdx.x >> 5) % KS, lo, hi);
-            if (i < min(b0 + p.a.batch, p.n_items) && lo < hi) {
-                c = lo;
+            p.share(w, lo, hi);
+            if (lo < hi) {
+                const int cw = w * (p.win / kChunkCols);
+                c = cw + lo * SC;
+                hi = cw + hi * SC;
                 const int lane = threadIdx.x & 31;
                 const int32_t item = p.items[i];
                 const int e = item_expert(item);
@@ -282,45 +314,52 @@ struct Loader {
                 const int rs = p.row(item, lane & 15);
                 on0 = r0 >= 0;
                 on1 = r1 >= 0;
-                ons = rs >= 0 && lane < 16;
-                const uint8_t *ce = p.codes + e * p.codes_e + (lane & 3) * 16 + lo * 64;
+                ons = rs >= 0;
+                const uint8_t *ce = p.codes + e * p.codes_e + (lane & 3) * 16 + c * 64;
                 src0 = ce + (int64_t)max(r0, 0) * (p.K32 / 2);
                 src1 = ce + (int64_t)max(r1, 0) * (p.K32 / 2);
                 const int q = max(rs, 0);
-                ssrc = p.scales + e * p.scales_e + ((int64_t)(q >> 7) * p.tk + lo) * kMx4Tile +
-                       (q & 31) * 16 + (q >> 5 & 3) * 4;
+                // lanes 0..15: the words of the stage's first chunk; 16..31: of its second
+                ssrc = p.scales + e * p.scales_e +
+                       ((int64_t)(q >> 7) * p.tk + c + (lane >> 4)) * kMx4Tile + (q & 31) * 16 +
+                       (q >> 5 & 3) * 4;
                 return;
             }
-            if (w + 1 < p.n_win) {
-                ++w;
-            } else {
-                b0 += p.a.batch;
-                w = 0;
-            }
-            i = b0 + grp();
+            next();
         }
     }
-    // issues the next chunk (if any) as one group
+    __device__ __forceinline__ void next()
+    {
+        if (++w == p.n_win) {
+            w = 0;
+            i += p.groups();
+        }
+    }
+    // issues the next stage (if any) as one group
     __device__ __forceinline__ void issue()
     {
-        if (b0 < p.n_items) {
+        if (i < p.n_items) {
             const int lane = threadIdx.x & 31;
-            // columns past K32 are zeros
-            const bool in = c * 64 + (lane & 3) * 16 < p.K32 / 2;
-            cp16(st + dst, src0, in && on0);
-            cp16(st + dst + 512, src1, in && on1);
-            if (lane < 16)
-                cp4(st + 1024 + lane * 4, ssrc, ons);
-            src0 += 64;
-            src1 += 64;
-            ssrc += kMx4Tile;
-            if (__builtin_expect(++c == hi, 0)) {
-                i += NG;
+#pragma unroll
+            for (int u = 0; u < SC; ++u) {  // columns past K32 are zeros
+                const bool in = (c + u) * 64 + (lane & 3) * 16 < p.K32 / 2;
+                cp16(st + u * kChunkBytes + dst, src0 + u * 64, in && on0);
+                cp16(st + u * kChunkBytes + dst + 512, src1 + u * 64, in && on1);
+            }
+            if (SC == 2 || lane < 16)
+                cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4, ssrc,
+                    ons && c + (lane >> 4) < p.tk);
+            src0 += SC * 64;
+            src1 += SC * 64;
+            ssrc += SC * kMx4Tile;
+            c += SC;
+            if (__builtin_expect(c == hi, 0)) {
+                next();
                 open();
             }
         }
         cp_commit();
-        st = st + kChunkBytes == ring + DEPTH * kChunkBytes ? ring : st + kChunkBytes;
+        st = st + SB == ring + DEPTH * SB ? ring : st + SB;
     }
 };
 
@@ -351,16 +390,15 @@ __device__ __forceinline__ float scale_chunk(uint4 &v)
     return mx4_scale(254u - field);
 }
 
-// Stages rows [0, n) of `cols` columns from column c0 (row j at src + j ld, columns below
-// `valid` exist; zeros up to a whole chunk) as scaled f16, inv[j * chunks + ch] the scales'
-// inverses.  With RAW the bf16 rows lie in the region already.  Called by warps
+// Stages rows [0, n), `chunks` chunks from column c0 (row j at src + j ld, columns below
+// `valid` exist, zeros past them) as scaled f16, inv[j * chunks + ch] the scales' inverses.  With RAW the bf16 rows lie in the region already.  Called by warps
 // [first, 16), each half warp one chunk of one row at a time.
 template <bool RAW>
 __device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, int n, int c0,
-                                           int cols, int valid, const bf16 *src, int64_t ld,
+                                           int chunks, int valid, const bf16 *src, int64_t ld,
                                            int first)
 {
-    const int chunks = (cols + kChunkCols - 1) / kChunkCols, total = n * chunks;
+    const int total = n * chunks;
     const int hw = ((int)threadIdx.x >> 4) - 2 * first, l = threadIdx.x & 15;
     const int step = 2 * (kWarps - first);
     constexpr int U = 4;
@@ -397,13 +435,20 @@ __device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, 
     }
 }
 
-// 2^s of byte b of a scale word.  The byte moves into the exponent field; 0 becomes 2^-127,
-// and 255 (infinity there) NaN by the multiplication with 0.
-__device__ __forceinline__ float word_scale(uint32_t w, int b)
+// 2^s of the four bytes of a scale word (0: 2^-127, 255: NaN, as the conversion has them)
+__device__ __forceinline__ void word_scales(uint32_t w, float (&s)[4])
 {
-    const uint32_t f = (b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7f800000u;
-    const float s = __uint_as_float(max(f, 0x00400000u));
-    return fmaf(s, 0.f, s);
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    s[0] = __uint_as_float(lo << 16);
+    s[1] = __uint_as_float(lo & 0xffff0000u);
+    s[2] = __uint_as_float(hi << 16);
+    s[3] = __uint_as_float(hi & 0xffff0000u);
 }
 
 // acc += (A chunk * B) * inv: the chunk's 16 rows (stage at `st`, this lane's words of row g
@@ -414,7 +459,9 @@ __device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, cons
                                           const uint32_t (&bp)[NB], const uint32_t (&ip)[NB][2],
                                           int g)
 {
-    const uint32_t w0 = lds32(st + 1024 + g * 4), w1 = lds32(st + 1056 + g * 4);
+    float s0[4], s1[4];
+    word_scales(lds32(st + 1024 + g * 4), s0);
+    word_scales(lds32(st + 1056 + g * 4), s1);
     float sum[NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -426,17 +473,16 @@ __device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, cons
         uint32_t a0[4], a1[4];
         mx4_halves8(lds32(st + off[b]), a0);
         mx4_halves8(lds32(st + off[b] + 512), a1);
-        const float s0 = word_scale(w0, b), s1 = word_scale(w1, b);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const uint4 x = lds128(bp[nb] + b * 64);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
             mma_f16(t, a0[0], a1[0], a0[1], a1[1], x.x, x.y);
             mma_f16(t, a0[2], a1[2], a0[3], a1[3], x.z, x.w);
-            sum[nb][0] = fmaf(t[0], s0, sum[nb][0]);
-            sum[nb][1] = fmaf(t[1], s0, sum[nb][1]);
-            sum[nb][2] = fmaf(t[2], s1, sum[nb][2]);
-            sum[nb][3] = fmaf(t[3], s1, sum[nb][3]);
+            sum[nb][0] = fmaf(t[0], s0[b], sum[nb][0]);
+            sum[nb][1] = fmaf(t[1], s0[b], sum[nb][1]);
+            sum[nb][2] = fmaf(t[2], s1[b], sum[nb][2]);
+            sum[nb][3] = fmaf(t[3], s1[b], sum[nb][3]);
         }
     }
 #pragma unroll
@@ -592,9 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     constexpr int RQ = 4 * NB;                      // sums of a lane
     char *region = sm;
     float *red = reinterpret_cast<float *>(sm + a.region);
+    constexpr int SB = stage_bytes(NB), SC = stage_chunks(NB);
     char *ring = sm + a.region + a.red;
-    float *outs = reinterpret_cast<float *>(ring + kWarps * DEPTH * kChunkBytes);
-    char *my_ring = ring + warp * DEPTH * kChunkBytes;
+    float *outs = reinterpret_cast<float *>(ring + kWarps * DEPTH * SB);
+    char *my_ring = ring + warp * DEPTH * SB;
     const int pitch1 = row_pitch(a.win1), pitch2 = row_pitch(a.win2);
     const uint32_t region_s = smem_u32(region), ring_s = smem_u32(my_ring);
     load_x(a, region_s, pitch1, 0, min(a.win1, d));
@@ -609,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
     switch ((nout + 7) / 8) {
-    case 1: router_logits<1>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
-    case 2: router_logits<2>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
-    case 3: router_logits<3>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
-    default: router_logits<4>(a, region, pitch1, my_ring, DEPTH * kChunkBytes, red, s_lg); break;
+    case 1: router_logits<1>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
+    case 2: router_logits<2>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
+    case 3: router_logits<3>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
+    default: router_logits<4>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
     }
     if (warp < T)
         gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
@@ -623,17 +670,35 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // ---- dispatch tables by warp 0 (lane e: expert e): stable by token, assignments past the
     // capacity dropped; the other warps turn the staged x into scaled f16
     const bool one_window = d <= a.win1;
+    const int chunks1 = (min(a.win1, d) + stage_cols(NB) - 1) / stage_cols(NB) * SC;
     if (warp == 0) {
-        int cnt = 0;
-        for (int i = 0; i < T * k; ++i)
-            cnt += s_idx[i] == lane;
-        cnt = lane < E ? cnt : 0;
+        constexpr int B = kMaxRows / 32;
+        const int n = T * k;
+        int v[B], rank[B], cnt = 0;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            v[b] = 32 * b + lane < n ? s_idx[32 * b + lane] : -1;
+            rank[b] = 0;
+        }
+        for (int e = 0; e < E; ++e) {
+            int base = 0;
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (32 * b >= n)
+                    break;
+                const uint32_t hit = __ballot_sync(0xffffffffu, v[b] == e);
+                if (v[b] == e)
+                    rank[b] = base + __popc(hit & ((1u << lane) - 1));
+                base += __popc(hit);
+            }
+            cnt = lane == e ? base : cnt;
+        }
         const int kept = a.C < 0 ? cnt : min(cnt, a.C);
         int off = kept;  // inclusive prefix sum
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, off, o);
-            off += lane >= o ? v : 0;
+            const int u = __shfl_up_sync(0xffffffffu, off, o);
+            off += lane >= o ? u : 0;
         }
         const uint32_t used = __ballot_sync(0xffffffffu, kept > 0);
         if (lane < E) {
@@ -647,20 +712,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             s_off[0] = 0;
             s_nsel = __popc(used);
         }
-        int row = off - kept, left = kept;
-        for (int i = lane; i < T * k; i += 32)
-            s_slot[i] = -1;
-        __syncwarp();
-        for (int t = 0; t < T; ++t)
-            for (int j = 0; j < k; ++j)  // a token names an expert once
-                if (s_idx[t * k + j] == lane && left > 0) {
-                    s_slot[t * k + j] = row;
-                    s_rtok[row] = t;
-                    ++row;
-                    --left;
-                }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (32 * b >= n)
+                break;
+            const int e = max(v[b], 0), i = 32 * b + lane;
+            const int first = __shfl_sync(0xffffffffu, off - kept, e);
+            const int room = __shfl_sync(0xffffffffu, kept, e);
+            const int row = v[b] >= 0 && rank[b] < room ? first + rank[b] : -1;
+            if (i < n)
+                s_slot[i] = row;
+            if (row >= 0)
+                s_rtok[row] = i / k;
+        }
     } else if (one_window) {
-        stage_rows<true>(region, pitch1, s_inv, T, 0, d, d, nullptr, 0, 1);
+        stage_rows<true>(region, pitch1, s_inv, T, 0, chunks1, d, nullptr, 0, 1);
     }
     __syncthreads();
     const int nsel = s_nsel, R = s_off[E], m8 = round_up(m, 8);
@@ -670,82 +736,92 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         a_off[b] = (uint32_t)(g * 64 + ((b ^ ((g >> 1) & 3)) << 4) + c * 4);
 
     // ---- one product phase over the table's items: their sums, handed to done(item, slot,
-    // sum) in the order of a thread's slots (PER threads per item), where sum(L, q) is value
-    // q of lane L
+    // sum) for PER slots an item, where sum(L, q) is value q of lane L.  A group's warps add
+    // their parts in warp order; groups wait for one another only to stage a window.
     auto products = [&](auto &ph, auto &ld, auto per, int pitch, bool staged, auto stage, auto brow,
                         auto done) {
         constexpr int PER = decltype(per)::value;
-        const int grp = warp / KS, ks = warp % KS;
+        const int grp = ph.group(), nks = 1 << ph.kshift, ks = warp & (nks - 1);
         uint32_t st = ring_s;
-        for (int b0 = 0; b0 < ph.n_items; b0 += a.batch) {
-            const int b1 = min(b0 + a.batch, ph.n_items);
+        float *part = red;  // two buffers in turn: one barrier an item
+        int buf = 0;
+#pragma unroll 1
+        for (int i0 = 0; i0 < ph.n_items; i0 += ph.groups()) {
+            const int i = i0 + grp;
+            const bool mine = i < ph.n_items;
+            const int32_t item = ph.items[mine ? i : 0];
+            float acc[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[nb][q] = 0.f;
+#pragma unroll 1
             for (int w = 0; w < ph.n_win; ++w) {
                 if (!staged || ph.n_win > 1) {
-                    if (b0 + w > 0)
+                    if (i0 + w > 0)
                         __syncthreads();  // the last window's products are done
                     stage(w);
                     __syncthreads();
                     staged = true;
                 }
+                if (!mine)
+                    continue;
                 int lo, hi;
-                ph.share(w, ks, lo, hi);
-                const int c0 = w * (ph.win / kChunkCols);
-                const int chunks = min(ph.win / kChunkCols, ph.tk - c0);
-                for (int i = b0 + grp; i < b1; i += NG) {
-                    uint32_t bp[NB], ip[NB][2];
-                    const int32_t item = ph.items[i];
+                ph.share(w, lo, hi);
+                const int chunks = ph.chunks(w);
+                uint32_t bp[NB], ip[NB][2];
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        bp[nb] = region_s + (uint32_t)(brow(item, nb * 8 + g) * pitch +
-                                                       (lo - c0) * kChunkCols * 2 + 16 * c);
+                for (int nb = 0; nb < NB; ++nb) {
+                    bp[nb] = region_s + (uint32_t)(brow(item, nb * 8 + g) * pitch +
+                                                   lo * stage_cols(NB) * 2 + 16 * c);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            ip[nb][j] = smem_u32(s_inv + brow(item, nb * 8 + 2 * c + j) * chunks +
-                                                 lo - c0);
-                    }
-                    float acc[NB][4];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[nb][q] = 0.f;
+                    for (int j = 0; j < 2; ++j)
+                        ip[nb][j] = smem_u32(s_inv + brow(item, nb * 8 + 2 * c + j) * chunks + lo * SC);
+                }
 #pragma unroll 1
-                    for (int ch = lo; ch < hi; ++ch) {
-                        __syncwarp();  // the stage the loader fills next has been read
-                        ld.issue();
-                        cp_wait<DEPTH - 1>();
-                        __syncwarp();
-                        chunk_mma<NB>(acc, st, a_off, bp, ip, g);
+                for (int n = hi - lo; n > 0; --n) {
+                    __syncwarp();  // the stage the loader fills next has been read
+                    ld.issue();
+                    cp_wait<DEPTH - 1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < SC; ++u) {
+                        chunk_mma<NB>(acc, st + u * kChunkBytes, a_off, bp, ip, g);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             bp[nb] += kChunkCols * 2;
                             ip[nb][0] += 4;
                             ip[nb][1] += 4;
                         }
-                        st = st + kChunkBytes == ring_s + DEPTH * kChunkBytes ? ring_s
-                                                                              : st + kChunkBytes;
                     }
-                    float *rw = red + ((size_t)((i - b0) * KS + ks) * 32 + lane) * RQ;
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            rw[nb * 4 + q] = w == 0 ? acc[nb][q] : rw[nb * 4 + q] + acc[nb][q];
+                    st = st + SB == ring_s + DEPTH * SB ? ring_s : st + SB;
                 }
             }
-            __syncthreads();
-            for (int j = threadIdx.x; j < (b1 - b0) * PER; j += kThreads) {
-                const int i = j / PER;
-                done(ph.items[b0 + i], j % PER, [&](int L, int q) {
-                    float v = 0.f;
+            if (!mine)
+                continue;
+            float *rw = part + ((size_t)(buf * kWarps + warp) * 32 + lane) * RQ;
 #pragma unroll
-                    for (int u = 0; u < KS; ++u)
-                        v += red[((size_t)(i * KS + u) * 32 + L) * RQ + q];
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    rw[nb * 4 + q] = acc[nb][q];
+            if (ph.kshift == 0)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(32 << ph.kshift) : "memory");
+            const float *r0 = part + (size_t)(buf * kWarps + (grp << ph.kshift)) * 32 * RQ;
+#pragma unroll 1
+            for (int j = ks * 32 + lane; j < PER; j += 32 << ph.kshift)
+                done(item, j, [&](int L, int q) {
+                    const float *r = r0 + (size_t)L * RQ + q;
+                    float v = 0.f;
+#pragma unroll 4
+                    for (int u = 0; u < nks; ++u)
+                        v += r[(size_t)u * 32 * RQ];
                     return v;
                 });
-            }
-            if (b1 < ph.n_items)
-                __syncthreads();  // the sums are read before the next batch's are written
+            buf ^= 1;
         }
     };
 
@@ -754,8 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     const int n_up = up.hi > up.lo ? up.count() : 0;
 #pragma unroll 1
     for (int base = 0; base < n_up; base += kItems) {
-        Phase<true> ph(a, s_items);
-        ph.n_items = min(kItems, n_up - base);
+        Phase<true, NB> ph(a, s_items);
+        ph.set(min(kItems, n_up - base));
         if (base > 0)
             __syncthreads();  // the table's last use is over
         if ((int)threadIdx.x < ph.n_items) {
@@ -764,12 +840,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
         }
         __syncthreads();
-        Loader<true, DEPTH> ld(ph, ring_s);
+        Loader<true, NB, DEPTH> ld(ph, ring_s);
         products(
             ph, ld, std::integral_constant<int, 64 * NB>(), pitch1, one_window,
             [&](int w) {
-                stage_rows<false>(region, pitch1, s_inv, T, w * a.win1,
-                                  min(a.win1, d - w * a.win1), d, a.x, d, 0);
+                stage_rows<false>(region, pitch1, s_inv, T, w * a.win1, ph.chunks(w), d, a.x, d, 0);
             },
             [&](int32_t item, int tok) {
                 const int e = item_expert(item), r0 = s_off[e];
@@ -793,9 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // and CTA 0 writes the routing, the tables and the statistics
     const DownItems down(d);
     const int n_down = nsel * down.per;
-    Phase<false> ph(a, s_items);
+    Phase<false, NB> ph(a, s_items);
     auto fill_down = [&](int base) {
-        ph.n_items = min(kItems, n_down - base);
+        ph.set(min(kItems, n_down - base));
         if ((int)threadIdx.x < ph.n_items) {
             int is, q, n;
             down.get(base + threadIdx.x, is, q, n);
@@ -814,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     }
     fill_down(0);
     __syncthreads();
-    Loader<false, DEPTH> ld(ph, ring_s);
+    Loader<false, NB, DEPTH> ld(ph, ring_s);
     if (threadIdx.x == 0) {
         const uint64_t t0 = globaltimer_ns();
         while (ld_acquire_gpu(a.gbar + 1) == gen) {
@@ -871,9 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             products(
                 ph, ld, std::integral_constant<int, 128 * NB>(), pitch2, base > 0,
                 [&](int w) {
-                    const int K = mx4_k32(m);
-                    stage_rows<false>(region, pitch2, s_inv, R, w * a.win2,
-                                      min(a.win2, K - w * a.win2), m, a.h, m8, 0);
+                    stage_rows<false>(region, pitch2, s_inv, R, w * a.win2, ph.chunks(w), m, a.h,
+                                      m8, 0);
                 },
                 [&](int32_t item, int tok) {
                     const int e = item_expert(item);
@@ -917,11 +991,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 // --------------------------------------------------------------------- host side
 
 constexpr int kDepths = 3;
-constexpr int kDepth[kDepths] = {6, 4, 2};  // chunks of a warp's ring
+constexpr int kDepth[kDepths] = {4, 3, 2};  // stages of a warp's ring
 typedef void (*Kernel)(const Args);
 static const Kernel kKernel[2][kDepths] = {
-    {mx4_few_kernel<1, 6>, mx4_few_kernel<1, 4>, mx4_few_kernel<1, 2>},
-    {mx4_few_kernel<2, 6>, mx4_few_kernel<2, 4>, mx4_few_kernel<2, 2>}};
+    {mx4_few_kernel<1, 4>, mx4_few_kernel<1, 3>, mx4_few_kernel<1, 2>},
+    {mx4_few_kernel<2, 4>, mx4_few_kernel<2, 3>, mx4_few_kernel<2, 2>}};
 
 static cudaError_t grid_size(int *out)
 {
@@ -951,14 +1025,14 @@ static cudaError_t grid_size(int *out)
 
 // Columns staged at once for `rows` activation rows of K columns: all of them if they fit
 // the region and the table of scales, else as many whole chunks as do.
-static int window(int rows, int K)
+static int window(int rows, int K, int nb)
 {
-    const int k128 = (K + kChunkCols - 1) / kChunkCols * kChunkCols;
-    int w = (kMaxRegion / rows - 64) / 2 / kChunkCols * kChunkCols;
+    const int unit = stage_cols(nb), all = (K + unit - 1) / unit * unit;
+    int w = (kMaxRegion / rows - 64) / 2;
     const int t = kMaxInv / rows * kChunkCols;
     w = w < t ? w : t;
-    w = w < kMaxWindow ? w : kMaxWindow;
-    return w < k128 ? w : k128;
+    w = (w < kMaxWindow ? w : kMaxWindow) / unit * unit;
+    return w < all ? w : all;
 }
 
 }  // namespace few
@@ -1013,18 +1087,17 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.C = p->capacity;
     a.router_type = p->router_type;
     const int R = p->T * p->k, nb = p->T <= 8 ? 1 : 2;
-    a.win1 = window(p->T, p->d);
-    a.win2 = window(R, p->m);
+    a.win1 = window(p->T, p->d, nb);
+    a.win2 = window(R, p->m, nb);
     const int x_bytes = p->T * row_pitch(a.win1), h_bytes = R * row_pitch(a.win2);
     a.region = round_up(x_bytes > h_bytes ? x_bytes : h_bytes, 128);
-    // 16 KB of partial sums a batch; the router's partial logits come there first
-    a.batch = nb == 1 ? 8 : 4;
+    // two buffers of the warps' sums; the router's partial logits come there first
     const int part = kWarps * p->T * round_up((b->Wnoise != nullptr ? 2 : 1) * p->E, 8) * 4;
-    a.red = a.batch * KS * 32 * 4 * nb * 4;
+    a.red = 2 * kWarps * 32 * 4 * nb * 4;
     a.red = round_up(a.red > part ? a.red : part, 128);
     const int64_t quads = (p->d + 127) / 128 * 32;
     const size_t outs = (size_t)R * 4 * ((quads + grid - 1) / grid + 1) * 4;
-    const size_t fixed = (size_t)a.region + a.red + outs, per = (size_t)kWarps * kChunkBytes;
+    const size_t fixed = (size_t)a.region + a.red + outs, per = (size_t)kWarps * stage_bytes(nb);
     int di = 0;
     while (di < kDepths && fixed + kDepth[di] * per > kSmemCap)
         ++di;
