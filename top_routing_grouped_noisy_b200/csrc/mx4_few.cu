@@ -11,22 +11,27 @@
 //             are some ten KB and no CTA waits for another.
 //   GEMM 1    the selected experts' neurons are split evenly over the CTAs; an item is 8
 //             neurons of one expert: their W1 rows are A rows 0..7 of mma.sync m16n8k16,
-//             their W3 rows A rows 8..15, the expert's tokens are B.
-//   GEMM 2    after a grid barrier (h complete): each CTA owns a range of output columns of
-//             every selected expert (items of 16 W2 rows), so the combine needs no other.
+//             their W3 rows A rows 8..15.  B is all of the batch's tokens, whatever the
+//             expert (8 columns cost what one does): a warp's slice of 256 columns stays in
+//             its registers for every item, and the epilogue keeps the routed tokens.
+//   GEMM 2    after a grid barrier (h complete): each CTA owns a strip of at most 32 output
+//             columns.  Column t of B is token t's row of h in the expert at hand; a warp
+//             walks over (expert, 128 columns of h) and adds gate weight * product to the
+//             same sums throughout, so one reduction ends in y.
 //
 // The product.  e2m1 values are exact in f16 (one conversion per pair), so A is the codes
-// themselves; B is the bf16 activations scaled by a power of two per row to a maximum in
-// [2^13, 2^14): exact in f16 down to 2^-27 of the row's maximum, off by less than 2^-38 of
-// it below.  The two products of a 32-column block accumulate in f32 and are added to the
-// sum times the block's scale, so the weights' scales may lie any distance apart.  A lane's
+// themselves; B is the bf16 activations scaled by a power of two per 128 columns to a maximum
+// in [2^13, 2^14): exact in f16 down to 2^-27 of that maximum, off by less than 2^-38 of it
+// below.  The two products of a 32-column block accumulate in f32 and are added to the sum
+// times the block's scale, so the weights' scales may lie any distance apart.  A lane's
 // k indexes are 8 consecutive columns, for A and B alike (the order of k inside a product
 // is free).
 //
-// Weights stream through a ring of chunks (16 rows x 128 columns and their 16 scale words)
-// that each warp fills for itself with cp.async, several chunks ahead and across items:
-// no barrier between loads and products but __syncwarp.  Four warps split the columns of
-// an item and four groups of them take the items in turn; partial sums meet in shared
+// Weights stream through a ring of stages (GEMM 1: 16 rows x 256 columns, GEMM 2: 32 x 128,
+// with their 32 scale words) that each warp fills for itself with cp.async, several stages
+// ahead and across items: no barrier between loads and products but __syncwarp.  The loop is
+// bound by the integer pipe (the conversions) and by shared-memory wavefronts, which is why B
+// stays in registers in GEMM 1 and serves 32 rows in GEMM 2.  Partial sums meet in shared
 // memory in warp order, so results do not depend on timing.
 //
 // Rows are enumerated in the order of the scale tiles (4 rows that lie 32 apart share 16
@@ -45,18 +50,17 @@ using tc::smem_u32;
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kChunkCols = 128;
-constexpr int kChunkBytes = 16 * 64 + 64;     // codes, scale words
-// chunks of a ring stage: two halve the loop's overhead per weight; with two groups of 8
-// tokens the staged activations leave room for single chunks only
-__host__ __device__ constexpr int stage_chunks(int nb) { return nb == 1 ? 2 : 1; }
-__host__ __device__ constexpr int stage_cols(int nb) { return stage_chunks(nb) * kChunkCols; }
-__host__ __device__ constexpr int stage_bytes(int nb) { return stage_chunks(nb) * kChunkBytes; }
+constexpr int kChunkBytes = 16 * 64 + 64;     // 16 rows x 128 columns: codes, scale words
+constexpr int kStageBytes = 2 * kChunkBytes;
+constexpr int kSlice = 256;                   // GEMM 1: columns of a warp
+constexpr int kWindow1 = kWarps * kSlice;     // columns of x at a time
+constexpr int kStrip = 32;                    // GEMM 2: output columns at a time
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
-constexpr int kMaxRegion = 136 * 1024;        // staged activations
-constexpr int kMaxWindow = 8192;              // columns staged at once
-constexpr int kMaxInv = 1088;                 // (row, chunk) scales of a window
-constexpr size_t kSmemCap = 212 * 1024;       // dynamic; the static tables take 12 KB
+constexpr int kSums = 64 * 1024;              // GEMM 1: the warps' sums of a batch of items
+constexpr int kMaxRegion = 96 * 1024;         // staged rows of h (or those sums)
+constexpr int kMaxInv = 1088;                 // (row, chunk) scales of a window of h
+constexpr size_t kSmemCap = 208 * 1024;       // dynamic; the static tables take 17 KB
 
 struct Args {
     const bf16 *x, *Wg, *Wn;
@@ -69,7 +73,7 @@ struct Args {
     uint64_t wait_ns;
     float lambda, scale;
     int T, d, m, E, k, C, router_type;
-    int region, red, win1, win2;  // bytes, bytes, columns staged
+    int region, win2;  // bytes; columns of h staged at once
 };
 
 // 16 or 4 bytes to shared memory; zeros where `on` is false (nothing is read then)
@@ -166,218 +170,252 @@ __device__ __forceinline__ int up_neuron(int q, int s)
 }
 
 // GEMM 2 works on quads of output columns, 32 quads per 128 columns: quad q is columns
-// 128 (q / 32) + q % 32 + 32 i.  A CTA takes quads [lo, hi) of every selected expert, four
-// per item.
-struct DownItems {
-    int lo, hi, per;  // per: items of an expert
-    __device__ __forceinline__ explicit DownItems(int d)
-    {
-        const uint32_t all = (uint32_t)((d + 127) / 128 * 32);
-        lo = (int)(blockIdx.x * all / gridDim.x);
-        hi = (int)((blockIdx.x + 1) * all / gridDim.x);
-        per = (hi - lo + 3) / 4;
-    }
-    __device__ __forceinline__ void get(int i, int &is, int &q, int &n) const
-    {
-        is = i / per;
-        q = lo + 4 * (i - is * per);
-        n = min(4, hi - q);
-    }
-};
+// 128 (q / 32) + q % 32 + 32 i.  A CTA takes quads [lo, hi), eight per strip; the s-th column
+// counted from quad q on:
 __device__ __forceinline__ int down_column(int q, int s)
 {
     const int qq = q + s / 4;
     return qq / 32 * 128 + qq % 32 + 32 * (s % 4);
 }
 
-// --------------------------------------------------------------------- one product phase
-// Items of a phase, at most kItems at a time, as a table in shared memory: expert, quads and
-// first quad packed into a word (the divisions behind them are made once per item, not by
-// every lane that loads or multiplies it).
+// --------------------------------------------------------------------- weight rings
+// GEMM 1's items, at most kItems at a time, as a table in shared memory: expert, quads and
+// first quad packed into a word (the divisions behind them are made once per item).
 constexpr int kItems = 512;
 __device__ __forceinline__ int32_t item_pack(int e, int q, int n) { return e | n << 5 | q << 8; }
 __device__ __forceinline__ int item_expert(int32_t v) { return v & 31; }
 __device__ __forceinline__ int item_quads(int32_t v) { return v >> 5 & 7; }
 __device__ __forceinline__ int item_first(int32_t v) { return v >> 8; }
 
-template <bool UP, int NB>
-struct Phase {
-    const Args &a;
-    const int32_t *items;
-    int n_items;                    // in the table
-    int kshift;                     // 2^kshift warps (a group) split the columns of an item
-    int K32, tk, win, n_win;
-    const uint8_t *codes, *scales;  // of all experts
-    int64_t codes_e, scales_e;      // bytes of an expert's
-    __device__ __forceinline__ Phase(const Args &args, const int32_t *table)
-        : a(args), items(table), n_items(0), kshift(0)
+// Scale word of row r, chunk c: its place in an expert's scales
+__device__ __forceinline__ int64_t word_at(int r, int c, int tk)
+{
+    return ((int64_t)(r >> 7) * tk + c) * kMx4Tile + (r & 31) * 16 + (r >> 5 & 3) * 4;
+}
+
+// How GEMM 1 is shared out: 2^kshift warps (a group) hold the slices of a window of x, the
+// groups take the items of a batch in turn.
+struct UpPlan {
+    int n, batch, kshift, n_win;  // items in the table; of a batch; ; windows
+    __device__ __forceinline__ UpPlan(int d, int nb)
     {
-        const int rows = UP ? 2 * round_up(a.m, 16) : a.d;
-        K32 = UP ? a.d : mx4_k32(a.m);
-        tk = (K32 + 127) / 128;
-        win = UP ? a.win1 : a.win2;
-        n_win = (K32 + win - 1) / win;
-        codes = UP ? a.W13q : a.W2q;
-        scales = UP ? a.W13s : a.W2s;
-        codes_e = (int64_t)rows * (K32 / 2);
-        scales_e = (int64_t)((rows + 127) / 128) * tk * kMx4Tile;
-    }
-    // For n items in the table: the split with the fewest stages on the busiest warp (the
-    // items go round the 16 / 2^kshift groups), the sum of an item's parts counted as half a
-    // stage.
-    __device__ __forceinline__ void set(int n)
-    {
-        n_items = n;
-        const int steps = n_win * ((min(win, K32) + stage_cols(NB) - 1) / stage_cols(NB));
-        int best = 1 << 30;
-#pragma unroll
-        for (int k = 0; k <= 4; ++k) {
-            const int cost = ((n + (kWarps >> k) - 1) >> (4 - k)) *
-                             (2 * ((steps + (1 << k) - 1) >> k) + (k > 0 ? 1 : 0));
-            if (cost < best) {
-                best = cost;
-                kshift = k;
-            }
-        }
-    }
-    // the row of the expert's matrix that A row r (0..15) of an item holds; -1: none
-    __device__ __forceinline__ int row(int32_t item, int r) const
-    {
-        const int q = item_first(item), n4 = 4 * item_quads(item);
-        if constexpr (UP) {
-            const int s = r & 7, nr = up_neuron(q, s);
-            return (s < n4 && nr < a.m) ? (nr >> 4) * 32 + (nr & 15) + (r >= 8 ? 16 : 0) : -1;
-        } else {
-            const int col = down_column(q, r);
-            return (r < n4 && col < a.d) ? col : -1;
-        }
-    }
-    // stages [lo, hi) of window w (counted inside it) that this warp takes
-    __device__ __forceinline__ void share(int w, int &lo, int &hi) const
-    {
-        const int n = (min(win, K32 - w * win) + stage_cols(NB) - 1) / stage_cols(NB);
-        const int ks = (int)(threadIdx.x >> 5) & ((1 << kshift) - 1);
-        lo = (ks * n) >> kshift;
-        hi = ((ks + 1) * n) >> kshift;
-    }
-    // chunks staged of window w: whole stages
-    __device__ __forceinline__ int chunks(int w) const
-    {
-        return (min(win, K32 - w * win) + stage_cols(NB) - 1) / stage_cols(NB) * stage_chunks(NB);
+        n = 0;
+        n_win = (d + kWindow1 - 1) / kWindow1;
+        const int slices = (min(d, kWindow1) + kSlice - 1) / kSlice;
+        kshift = 32 - __clz(slices - 1);  // 0 for one slice
+        batch = kSums / (nb * 512) >> kshift;
     }
     __device__ __forceinline__ int group() const { return (int)(threadIdx.x >> 5) >> kshift; }
     __device__ __forceinline__ int groups() const { return kWarps >> kshift; }
+    // first column of this warp's slice of window w
+    __device__ __forceinline__ int column(int w) const
+    {
+        return w * kWindow1 + ((int)(threadIdx.x >> 5) & ((1 << kshift) - 1)) * kSlice;
+    }
 };
 
-// Loader state of one warp: the stages of a phase's table in the order the products take
-// them: the group's items, windows of columns, the warp's stages.
-template <bool UP, int NB, int DEPTH>
-struct Loader {
-    static constexpr int SB = stage_bytes(NB), SC = stage_chunks(NB);
-    const Phase<UP, NB> &p;
-    uint32_t ring, st, dst;  // this warp's stages, the next one, this lane's place in it
-    int w, i, c, hi;         // c: first chunk of the next stage; hi: end of the warp's share
-    const uint8_t *src0, *src1, *ssrc;  // this lane's 16-byte pieces (two rows), its scale word
-    bool on0, on1, ons;
-    __device__ __forceinline__ Loader(const Phase<UP, NB> &ph, uint32_t r)
-        : p(ph), ring(r), w(0)
+// Loader of GEMM 1, one warp's: a stage is 16 rows (an item) x the 256 columns of the warp's
+// slice; order: batches of items, windows, the group's items.
+template <int DEPTH>
+struct UpLoader {
+    const Args &a;
+    const UpPlan &p;
+    const int32_t *items;
+    uint32_t ring, st, dst;
+    int b0, w, i;
+    __device__ __forceinline__ UpLoader(const Args &args, const UpPlan &plan, const int32_t *table,
+                                        uint32_t r)
+        : a(args), p(plan), items(table), ring(r), st(r), b0(0), w(0), i(plan.group())
     {
         const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
         dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-        restart();
-    }
-    // from the start of a (refilled) table: the first stages of the ring
-    __device__ __forceinline__ void restart()
-    {
-        w = 0;
-        st = ring;
-        i = p.group();
-        open();
+        skip();
 #pragma unroll 1
         for (int n = 0; n < DEPTH - 1; ++n)
             issue();
     }
-    // moves to the first item and window from (i, w) on that has a stage
-    __device__ __forceinline__ void open()
+    // past the ends of batches and windows, to an item of this group or to the end
+    __device__ __forceinline__ void skip()
     {
-        while (i < p.n_items) {
-            int lo;
-            p.share(w, lo, hi);
-            if (lo < hi) {
-                const int cw = w * (p.win / kChunkCols);
-                c = cw + lo * SC;
-                hi = cw + hi * SC;
-                const int lane = threadIdx.x & 31;
-                const int32_t item = p.items[i];
-                const int e = item_expert(item);
-                const int r0 = p.row(item, lane >> 2), r1 = p.row(item, (lane >> 2) + 8);
-                const int rs = p.row(item, lane & 15);
-                on0 = r0 >= 0;
-                on1 = r1 >= 0;
-                ons = rs >= 0;
-                const uint8_t *ce = p.codes + e * p.codes_e + (lane & 3) * 16 + c * 64;
-                src0 = ce + (int64_t)max(r0, 0) * (p.K32 / 2);
-                src1 = ce + (int64_t)max(r1, 0) * (p.K32 / 2);
-                const int q = max(rs, 0);
-                // lanes 0..15: the words of the stage's first chunk; 16..31: of its second
-                ssrc = p.scales + e * p.scales_e +
-                       ((int64_t)(q >> 7) * p.tk + c + (lane >> 4)) * kMx4Tile + (q & 31) * 16 +
-                       (q >> 5 & 3) * 4;
-                return;
+        while (b0 < p.n && i >= min(b0 + p.batch, p.n)) {
+            if (++w == p.n_win) {
+                w = 0;
+                b0 += p.batch;
             }
-            next();
+            i = b0 + p.group();
         }
     }
-    __device__ __forceinline__ void next()
+    // row of the expert's W13 that A row r of an item holds; -1: none
+    __device__ __forceinline__ int row(int32_t item, int r) const
     {
-        if (++w == p.n_win) {
-            w = 0;
-            i += p.groups();
-        }
+        const int s = r & 7, nr = up_neuron(item_first(item), s);
+        return (s < 4 * item_quads(item) && nr < a.m) ? (nr >> 4) * 32 + (nr & 15) + (r >= 8 ? 16 : 0)
+                                                       : -1;
     }
-    // issues the next stage (if any) as one group
     __device__ __forceinline__ void issue()
     {
-        if (i < p.n_items) {
+        if (b0 < p.n) {
             const int lane = threadIdx.x & 31;
-#pragma unroll
-            for (int u = 0; u < SC; ++u) {  // columns past K32 are zeros
-                const bool in = (c + u) * 64 + (lane & 3) * 16 < p.K32 / 2;
-                cp16(st + u * kChunkBytes + dst, src0 + u * 64, in && on0);
-                cp16(st + u * kChunkBytes + dst + 512, src1 + u * 64, in && on1);
-            }
-            if (SC == 2 || lane < 16)
-                cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4, ssrc,
-                    ons && c + (lane >> 4) < p.tk);
-            src0 += SC * 64;
-            src1 += SC * 64;
-            ssrc += SC * kMx4Tile;
-            c += SC;
-            if (__builtin_expect(c == hi, 0)) {
-                next();
-                open();
-            }
+            const int32_t item = items[i];
+            const int rows = 2 * round_up(a.m, 16), tk = (a.d + 127) >> 7, col = p.column(w);
+            const uint8_t *ce = a.W13q + (int64_t)(item_expert(item) * rows) * (a.d / 2);
+            const uint8_t *se = a.W13s + (int64_t)(item_expert(item) * ((rows + 127) >> 7)) * tk * kMx4Tile;
+            const int r0 = row(item, lane >> 2), r1 = row(item, (lane >> 2) + 8);
+            const int at = col / 2 + (lane & 3) * 16;  // columns past d are zeros
+            const uint8_t *s0 = ce + (int64_t)max(r0, 0) * (a.d / 2) + at;
+            const uint8_t *s1 = ce + (int64_t)max(r1, 0) * (a.d / 2) + at;
+            const bool in0 = at < a.d / 2, in1 = at + 64 < a.d / 2;
+            cp16(st + dst, s0, in0 && r0 >= 0);
+            cp16(st + dst + 512, s1, in0 && r1 >= 0);
+            cp16(st + kChunkBytes + dst, in1 ? s0 + 64 : s0, in1 && r0 >= 0);
+            cp16(st + kChunkBytes + dst + 512, in1 ? s1 + 64 : s1, in1 && r1 >= 0);
+            // lanes 0..15: the words of the first chunk; 16..31: of the second
+            const int rs = row(item, lane & 15), ch = (col >> 7) + (lane >> 4);
+            const bool ins = rs >= 0 && ch < tk;
+            cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4,
+                se + (ins ? word_at(rs, ch, tk) : 0), ins);
+            i += p.groups();
+            skip();
         }
         cp_commit();
-        st = st + SB == ring + DEPTH * SB ? ring : st + SB;
+        st = st + kStageBytes == ring + DEPTH * kStageBytes ? ring : st + kStageBytes;
     }
 };
 
-// One chunk (128 columns) of one staged row, 16 lanes with 8 bf16 columns each, as f16 scaled
-// by a power of two to a maximum in [2^13, 2^14); returns the scale's inverse.
-__device__ __forceinline__ float scale_chunk(uint4 &v)
+// How GEMM 2 is shared out: the (selected expert, chunk) pairs of a window of h go round the
+// warps.
+struct DownPlan {
+    int lo, hi, strips, nsel, K32, tk, win, n_win;
+    __device__ __forceinline__ DownPlan(const Args &a, int sel)
+    {
+        const uint32_t all = (uint32_t)((a.d + 127) / 128 * 32);
+        lo = (int)(blockIdx.x * all / gridDim.x);
+        hi = (int)((blockIdx.x + 1) * all / gridDim.x);
+        strips = (4 * (hi - lo) + kStrip - 1) / kStrip;
+        nsel = sel;
+        K32 = mx4_k32(a.m);
+        tk = (K32 + 127) >> 7;
+        win = a.win2 >> 7;  // in chunks
+        n_win = (tk + win - 1) / win;
+    }
+    __device__ __forceinline__ int chunks(int w) const { return min(win, tk - w * win); }
+};
+// the warp's place in the pairs of a window: expert is (among the selected), chunk c
+struct DownAt {
+    int is, c;
+    __device__ __forceinline__ void set(int n, int chunks)
+    {
+        is = n / chunks;
+        c = n - is * chunks;
+    }
+    __device__ __forceinline__ void step(int chunks)
+    {
+        c += kWarps;
+        while (c >= chunks) {
+            c -= chunks;
+            ++is;
+        }
+    }
+};
+
+// Loader of GEMM 2, one warp's: a stage is the strip's 32 rows x one chunk; order: strips,
+// windows, the warp's pairs.
+template <int DEPTH>
+struct DownLoader {
+    const Args &a;
+    const DownPlan &p;
+    const int32_t *sel;
+    uint32_t ring, st, dst;
+    int strip, w;
+    DownAt at;
+    int64_t off[4], soff;  // this lane's pieces of rows (lane / 4) + 8 i, its scale word
+    bool on[4], ons;
+    __device__ __forceinline__ DownLoader(const Args &args, const DownPlan &plan,
+                                          const int32_t *selected, uint32_t r)
+        : a(args), p(plan), sel(selected), ring(r), st(r), strip(0), w(0)
+    {
+        const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
+        dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+        open();
+        at.set((int)threadIdx.x >> 5, p.chunks(0));
+        skip();
+#pragma unroll 1
+        for (int n = 0; n < DEPTH - 1; ++n)
+            issue();
+    }
+    __device__ __forceinline__ int column(int r) const
+    {
+        const int q = p.lo + 8 * strip, col = down_column(q, r);
+        return r < 4 * (p.hi - q) && col < a.d ? col : -1;
+    }
+    // the rows of a strip
+    __device__ __forceinline__ void open()
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col = column((lane >> 2) + 8 * i);
+            on[i] = col >= 0;
+            off[i] = (int64_t)max(col, 0) * (p.K32 / 2) + (lane & 3) * 16;
+        }
+        const int col = column(lane);
+        ons = col >= 0;
+        soff = word_at(max(col, 0), 0, p.tk);
+    }
+    // past the ends of windows and strips
+    __device__ __forceinline__ void skip()
+    {
+        while (strip < p.strips && at.is >= p.nsel) {
+            if (++w == p.n_win) {
+                w = 0;
+                if (++strip < p.strips)
+                    open();
+            }
+            at.set((int)threadIdx.x >> 5, p.chunks(w));
+            if (p.nsel == 0)
+                strip = p.strips;
+        }
+    }
+    __device__ __forceinline__ void issue()
+    {
+        if (strip < p.strips) {
+            const int lane = threadIdx.x & 31, e = sel[at.is], c = w * p.win + at.c;
+            const uint8_t *ce = a.W2q + (int64_t)e * a.d * (p.K32 / 2) + c * 64;
+            const bool in = c * 64 + (lane & 3) * 16 < p.K32 / 2;  // columns past K32 are zeros
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool ok = in && on[i];
+                cp16(st + (i >> 1) * kChunkBytes + (i & 1) * 512 + dst, ok ? ce + off[i] : a.W2q, ok);
+            }
+            const uint8_t *se = a.W2s + (int64_t)(e * ((a.d + 127) >> 7)) * p.tk * kMx4Tile;
+            cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4, se + soff + (int64_t)c * kMx4Tile,
+                ons);
+            at.step(p.chunks(w));
+            skip();
+        }
+        cp_commit();
+        st = st + kStageBytes == ring + DEPTH * kStageBytes ? ring : st + kStageBytes;
+    }
+};
+
+// --------------------------------------------------------------------- activations
+// The power of two that takes a maximum with the bf16 magnitude bits `top` into [2^13, 2^14):
+// 2^(13 - floor(log2(max))), exponent field 127 + 13 - (E - 127), at most 254.
+__device__ __forceinline__ uint32_t scale_field(uint32_t top) { return min(267u - (top >> 7), 254u); }
+
+__device__ __forceinline__ uint32_t top_of(const uint4 &v)
 {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^(13 - floor(log2(max))): exponent field 127 + 13 - (E - 127), at most 254
-    const uint32_t field = min(267u - (top >> 7), 254u);
-    const float mul = __uint_as_float(field << 23);
+    return top;
+}
+
+// 8 bf16 values times mul, as f16
+__device__ __forceinline__ void to_half(uint4 &v, float mul)
+{
     float f[8];
     bf16x8_to_f32(v, f);
     uint32_t o[4];
@@ -387,35 +425,68 @@ __device__ __forceinline__ float scale_chunk(uint4 &v)
         o[i] = *reinterpret_cast<const uint32_t *>(&hh);
     }
     v = make_uint4(o[0], o[1], o[2], o[3]);
-    return mx4_scale(254u - field);
+}
+
+// GEMM 1's B: columns [col, col + 256) of every token as scaled f16 (lane (g, c): tokens g and
+// g + 8, 8 columns of each of the 8 blocks) and the scales' inverses of tokens 2c, 2c + 1.
+template <int NB>
+__device__ __forceinline__ void load_slice(const Args &a, int col, uint4 (&xb)[NB][8],
+                                           float (&inv)[NB][2][2])
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int t = nb * 8 + g;
+        const bf16 *src = a.x + (int64_t)t * a.d + col + 8 * c;
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            xb[nb][b] = (t < a.T && col + 32 * b < a.d) ? ld_nc(src + 32 * b) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                top = max(top, top_of(xb[nb][4 * u + b]));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t field = scale_field(top);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                to_half(xb[nb][4 * u + b], __uint_as_float(field << 23));
+            const float r = mx4_scale(254u - field);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                inv[nb][u][j] = __shfl_sync(0xffffffffu, r, (2 * c + j) * 4);
+        }
 }
 
 // Stages rows [0, n), `chunks` chunks from column c0 (row j at src + j ld, columns below
-// `valid` exist, zeros past them) as scaled f16, inv[j * chunks + ch] the scales' inverses.  With RAW the bf16 rows lie in the region already.  Called by warps
-// [first, 16), each half warp one chunk of one row at a time.
-template <bool RAW>
+// `valid` exist, zeros past them) as scaled f16; inv[j * chunks + ch]: the scales' inverses
+// times weight[j].  Called by the whole CTA, each half warp one chunk of one row at a time.
 __device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, int n, int c0,
                                            int chunks, int valid, const bf16 *src, int64_t ld,
-                                           int first)
+                                           const float *weight)
 {
     const int total = n * chunks;
-    const int hw = ((int)threadIdx.x >> 4) - 2 * first, l = threadIdx.x & 15;
-    const int step = 2 * (kWarps - first);
-    constexpr int U = 4;
+    const int hw = (int)threadIdx.x >> 4, l = threadIdx.x & 15;
+    constexpr int U = 4, step = 2 * kWarps;
 #pragma unroll 1
     for (int i0 = hw & ~1; i0 < total; i0 += U * step) {  // both halves of a warp loop alike
         uint4 v[U];
-        int at[U];
+        int at[U], row[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + (hw & 1) + u * step;
             const int j = i / chunks, col = (i - j * chunks) * kChunkCols + 8 * l;
             at[u] = i < total ? j * pitch + col * 2 : -1;
+            row[u] = j;
             v[u] = make_uint4(0, 0, 0, 0);
             if (i < total && c0 + col < valid)
-                v[u] = RAW ? *reinterpret_cast<const uint4 *>(region + at[u])
-                           : __ldcg(reinterpret_cast<const uint4 *>(src + j * ld + c0 + col));
-            if (!RAW && c0 + col + 8 > valid) {  // columns past the row's end hold anything
+                v[u] = __ldcg(reinterpret_cast<const uint4 *>(src + j * ld + c0 + col));
+            if (c0 + col + 8 > valid) {  // columns past the row's end hold anything
                 uint16_t *e = reinterpret_cast<uint16_t *>(&v[u]);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -425,11 +496,16 @@ __device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, 
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float r = scale_chunk(v[u]);
+            uint32_t top = top_of(v[u]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t field = scale_field(top);
+            to_half(v[u], __uint_as_float(field << 23));
             if (at[u] >= 0) {
                 st_v4(region + at[u], v[u]);
                 if (l == 0)
-                    inv[i0 + (hw & 1) + u * step] = r;
+                    inv[i0 + (hw & 1) + u * step] = mx4_scale(254u - field) * weight[row[u]];
             }
         }
     }
@@ -451,18 +527,15 @@ __device__ __forceinline__ void word_scales(uint32_t w, float (&s)[4])
     s[3] = __uint_as_float(hi & 0xffff0000u);
 }
 
-// acc += (A chunk * B) * inv: the chunk's 16 rows (stage at `st`, this lane's words of row g
-// at off[b]) against the token rows at the shared addresses bp[nb] (this lane's B row and 8
-// columns); inv[nb][j]: the scale of the row of token 2c + j.
-template <int NB>
-__device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, const uint32_t (&off)[4],
-                                          const uint32_t (&bp)[NB], const uint32_t (&ip)[NB][2],
-                                          int g)
+// sum = A chunk * B: the chunk's 16 rows (at `st`, this lane's words of row g at off[b])
+// against this lane's B fragments x[nb][b].
+template <int NB, class X>
+__device__ __forceinline__ void chunk_mma(float (&sum)[NB][4], uint32_t st, const uint32_t (&off)[4],
+                                          const X &x, int g)
 {
     float s0[4], s1[4];
     word_scales(lds32(st + 1024 + g * 4), s0);
     word_scales(lds32(st + 1056 + g * 4), s1);
-    float sum[NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -475,109 +548,32 @@ __device__ __forceinline__ void chunk_mma(float (&acc)[NB][4], uint32_t st, cons
         mx4_halves8(lds32(st + off[b] + 512), a1);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const uint4 x = lds128(bp[nb] + b * 64);
+            const uint4 v = x(nb, b);
             float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(t, a0[0], a1[0], a0[1], a1[1], x.x, x.y);
-            mma_f16(t, a0[2], a1[2], a0[3], a1[3], x.z, x.w);
+            mma_f16(t, a0[0], a1[0], a0[1], a1[1], v.x, v.y);
+            mma_f16(t, a0[2], a1[2], a0[3], a1[3], v.z, v.w);
             sum[nb][0] = fmaf(t[0], s0[b], sum[nb][0]);
             sum[nb][1] = fmaf(t[1], s0[b], sum[nb][1]);
             sum[nb][2] = fmaf(t[2], s1[b], sum[nb][2]);
             sum[nb][3] = fmaf(t[3], s1[b], sum[nb][3]);
         }
     }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const float i0 = __uint_as_float(lds32(ip[nb][0])), i1 = __uint_as_float(lds32(ip[nb][1]));
-        acc[nb][0] = fmaf(sum[nb][0], i0, acc[nb][0]);
-        acc[nb][1] = fmaf(sum[nb][1], i1, acc[nb][1]);
-        acc[nb][2] = fmaf(sum[nb][2], i0, acc[nb][2]);
-        acc[nb][3] = fmaf(sum[nb][3], i1, acc[nb][3]);
-    }
 }
 
 // --------------------------------------------------------------------- the router
-// Adds the 32-column steps [s_lo, s_hi) of a window whose bf16 rows lie in the region (step
-// 0 at its start, at global column c0) into acc: the warp's rows of [W_g | W_noise] go to its
-// own `stage` bytes, as many steps at a time as fit.
+// The logits lg [T][nout] of all tokens: warp w takes the 32-column steps [w S / 16,
+// (w + 1) S / 16), eight at a time, with its rows of [W_g | W_noise] in its own `stage`
+// bytes; the warps' sums (`part`) are added in warp order.
 template <int NT>
-__device__ __forceinline__ void router_steps(const Args &a, uint32_t rows, int pitch, int c0,
-                                             int s_lo, int s_hi, char *stage, int stage_bytes,
-                                             float (&acc)[NT][4])
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int E = a.E, T = a.T, nout = a.Wn != nullptr ? 2 * E : E;
-    constexpr int NP = NT * 8;
-    const int round = stage_bytes / (32 * NP * 2);
-    const uint32_t sb = smem_u32(stage);
-#pragma unroll 1
-    for (int s0 = s_lo; s0 < s_hi; s0 += round) {
-        const int n = min(round, s_hi - s0);
-        const int64_t k0 = c0 + s0 * 32;
-        __syncwarp();
-        if ((E & 7) == 0) {  // rows of whole 16-byte pieces
-            constexpr int PR = NT;
-#pragma unroll 4
-            for (int i = lane; i < n * 32 * PR; i += 32) {
-                const int k = i / PR, o = (i % PR) * 8;
-                const bf16 *src = o < E ? a.Wg + (k0 + k) * E + o : a.Wn + (k0 + k) * E + o - E;
-                cp16(sb + i * 16, src, true);
-            }
-            cp_commit();
-            cp_wait<0>();
-        } else {
-            const bf16 zero = __float2bfloat16_rn(0.f);
-#pragma unroll 4
-            for (int i = lane; i < n * 32 * NP; i += 32) {
-                const int k = i / NP, o = i % NP;
-                reinterpret_cast<bf16 *>(stage)[i] =
-                    o < E ? a.Wg[(k0 + k) * E + o]
-                          : (o < nout ? a.Wn[(k0 + k) * E + o - E] : zero);
-            }
-        }
-        __syncwarp();
-#pragma unroll 2
-        for (int s = 0; s < n; ++s) {
-            // A: 8 consecutive columns of token rows g, g + 8; B of the two products:
-            // columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
-            const uint32_t xa = rows + (uint32_t)(g * pitch + ((s0 + s) * 32 + 8 * c) * 2);
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            const uint4 x0 = g < T ? lds128(xa) : z;
-            const uint4 x1 = g + 8 < T ? lds128(xa + 8 * pitch) : z;
-            const int i = lane & 7, kk = s * 32 + 8 * (i >> 1) + (i & 1) + 2 * (lane >> 3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint32_t b[4];
-                ldsm_x4_trans(sb + (uint32_t)(kk * NP * 2 + nt * 16), b);
-                mma_bf16_16816(acc[nt], x0.x, x1.x, x0.y, x1.y, b[0], b[1]);
-                mma_bf16_16816(acc[nt], x0.z, x1.z, x0.w, x1.w, b[2], b[3]);
-            }
-        }
-    }
-}
-
-// Copies columns [c0, c0 + cols) of x's rows into the region as they are (asynchronous, one
-// group per thread).
-__device__ __forceinline__ void load_x(const Args &a, uint32_t region, int pitch, int c0, int cols)
-{
-    const int nv = cols / 8;
-#pragma unroll 1
-    for (int t = 0; t < a.T; ++t)
-#pragma unroll 2
-        for (int v = threadIdx.x; v < nv; v += kThreads)
-            cp16(region + (uint32_t)(t * pitch + v * 16), a.x + (int64_t)t * a.d + c0 + v * 8, true);
-    cp_commit();
-}
-
-// The logits lg [T][nout] of all tokens: in every window of x, warp w takes the w-th
-// sixteenth of the 32-column steps; the warps' sums are added in warp order.  With one window
-// the region is left holding x.
-template <int NT>
-__device__ __noinline__ void router_logits(const Args &a, char *region, int pitch, char *stage,
-                                           int stage_bytes, float *part, float *lg)
+__device__ __noinline__ void router_logits(const Args &a, char *stage, int stage_bytes, float *part,
+                                           float *lg)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int T = a.T, nout = a.Wn != nullptr ? 2 * a.E : a.E;
+    const int E = a.E, T = a.T, d = a.d, nout = a.Wn != nullptr ? 2 * E : E;
     constexpr int NP = NT * 8;
+    const int round = min(8, stage_bytes / (32 * NP * 2));
+    const uint32_t sb = smem_u32(stage);
+    const int steps = d / 32, s_hi = (warp + 1) * steps / kWarps;
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -585,16 +581,53 @@ __device__ __noinline__ void router_logits(const Args &a, char *region, int pitc
         for (int q = 0; q < 4; ++q)
             acc[nt][q] = 0.f;
 #pragma unroll 1
-    for (int c0 = 0; c0 < a.d; c0 += a.win1) {
-        const int cols = min(a.win1, a.d - c0), steps = cols / 32;
-        if (c0 > 0) {
-            __syncthreads();  // the last window's rows have been read
-            load_x(a, smem_u32(region), pitch, c0, cols);
+    for (int s0 = warp * steps / kWarps; s0 < s_hi; s0 += round) {
+        const int n = min(round, s_hi - s0);
+        const int64_t k0 = s0 * 32;
+        __syncwarp();
+        if ((E & 7) == 0) {  // rows of whole 16-byte pieces
+#pragma unroll 4
+            for (int i = lane; i < n * 32 * NT; i += 32) {
+                const int k = i / NT, o = (i % NT) * 8;
+                const bf16 *src = o < E ? a.Wg + (k0 + k) * E + o : a.Wn + (k0 + k) * E + o - E;
+                cp16(sb + i * 16, src, true);
+            }
+            cp_commit();
+        }
+        // A: 8 consecutive columns of token rows g, g + 8
+        uint4 x0[8], x1[8];
+        const bf16 *xs = a.x + (int64_t)g * d + k0 + 8 * c;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            x0[s] = s < n && g < T ? ld_nc(xs + s * 32) : make_uint4(0, 0, 0, 0);
+            x1[s] = s < n && g + 8 < T ? ld_nc(xs + (int64_t)8 * d + s * 32) : make_uint4(0, 0, 0, 0);
+        }
+        if ((E & 7) != 0) {
+            const bf16 zero = __float2bfloat16_rn(0.f);
+#pragma unroll 8
+            for (int i = lane; i < n * 32 * NP; i += 32) {
+                const int k = i / NP, o = i % NP;
+                reinterpret_cast<bf16 *>(stage)[i] =
+                    o < E ? a.Wg[(k0 + k) * E + o]
+                          : (o < nout ? a.Wn[(k0 + k) * E + o - E] : zero);
+            }
         }
         cp_wait<0>();
-        __syncthreads();
-        router_steps<NT>(a, smem_u32(region), pitch, c0, warp * steps / kWarps,
-                         (warp + 1) * steps / kWarps, stage, stage_bytes, acc);
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s >= n)
+                break;
+            // B of the two products: columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
+            const int i = lane & 7, kk = s * 32 + 8 * (i >> 1) + (i & 1) + 2 * (lane >> 3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t b[4];
+                ldsm_x4_trans(sb + (uint32_t)(kk * NP * 2 + nt * 16), b);
+                mma_bf16_16816(acc[nt], x0[s].x, x1[s].x, x0[s].y, x1[s].y, b[0], b[1]);
+                mma_bf16_16816(acc[nt], x0[s].z, x1[s].z, x0[s].w, x1[s].w, b[2], b[3]);
+            }
+        }
     }
     float *pw = part + (size_t)warp * T * NP;
 #pragma unroll
@@ -627,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     extern __shared__ __align__(128) char sm[];
     __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE], s_cnt[kMaxE], s_kept[kMaxE];
     __shared__ int32_t s_idx[kMaxRows], s_slot[kMaxRows], s_rtok[kMaxRows];
-    __shared__ float s_w[kMaxRows], s_inv[kMaxInv];
+    __shared__ int8_t s_map[kMaxE * MOE_MX4_FEW_TOKENS];  // row of (expert, token), -1 none
+    __shared__ float s_w[kMaxRows], s_rw[kMaxRows], s_inv[kMaxInv];
     __shared__ float s_lg[MOE_MX4_FEW_TOKENS * 32], s_prob[MOE_MX4_FEW_TOKENS * kMaxE],
         s_gw[MOE_MX4_FEW_TOKENS * kMaxE];
     __shared__ int32_t s_items[kItems];
@@ -635,16 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int T = a.T, E = a.E, k = a.k, d = a.d, m = a.m;
-    constexpr int RQ = 4 * NB;                      // sums of a lane
-    char *region = sm;
-    float *red = reinterpret_cast<float *>(sm + a.region);
-    constexpr int SB = stage_bytes(NB), SC = stage_chunks(NB);
-    char *ring = sm + a.region + a.red;
-    float *outs = reinterpret_cast<float *>(ring + kWarps * DEPTH * SB);
-    char *my_ring = ring + warp * DEPTH * SB;
-    const int pitch1 = row_pitch(a.win1), pitch2 = row_pitch(a.win2);
-    const uint32_t region_s = smem_u32(region), ring_s = smem_u32(my_ring);
-    load_x(a, region_s, pitch1, 0, min(a.win1, d));
+    char *region = sm;  // the router's sums, GEMM 1's, then the rows of h
+    char *my_ring = sm + a.region + warp * DEPTH * kStageBytes;
+    const uint32_t ring_s = smem_u32(my_ring);
     // the grid barrier's generation before this launch's barrier (it changes only once
     // every CTA has arrived, this one included)
     int32_t gen = 0;
@@ -652,14 +679,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         s_abort = 0;
         gen = ld_acquire_gpu(a.gbar + 1);
     }
+    for (int i = threadIdx.x; i < E * MOE_MX4_FEW_TOKENS; i += kThreads)
+        s_map[i] = -1;
 
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
+    float *part = reinterpret_cast<float *>(region);
     switch ((nout + 7) / 8) {
-    case 1: router_logits<1>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
-    case 2: router_logits<2>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
-    case 3: router_logits<3>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
-    default: router_logits<4>(a, region, pitch1, my_ring, DEPTH * SB, red, s_lg); break;
+    case 1: router_logits<1>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
+    case 2: router_logits<2>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
+    case 3: router_logits<3>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
+    default: router_logits<4>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
     }
     if (warp < T)
         gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
@@ -668,9 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                         a.status);
     __syncthreads();
     // ---- dispatch tables by warp 0 (lane e: expert e): stable by token, assignments past the
-    // capacity dropped; the other warps turn the staged x into scaled f16
-    const bool one_window = d <= a.win1;
-    const int chunks1 = (min(a.win1, d) + stage_cols(NB) - 1) / stage_cols(NB) * SC;
+    // capacity dropped
     if (warp == 0) {
         constexpr int B = kMaxRows / 32;
         const int n = T * k;
@@ -722,11 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             const int row = v[b] >= 0 && rank[b] < room ? first + rank[b] : -1;
             if (i < n)
                 s_slot[i] = row;
-            if (row >= 0)
-                s_rtok[row] = i / k;
+            if (row >= 0) {
+                const int t = i / k;
+                s_rtok[row] = t;
+                s_rw[row] = s_w[i];
+                s_map[e * MOE_MX4_FEW_TOKENS + t] = (int8_t)row;
+            }
         }
-    } else if (one_window) {
-        stage_rows<true>(region, pitch1, s_inv, T, 0, chunks1, d, nullptr, 0, 1);
     }
     __syncthreads();
     const int nsel = s_nsel, R = s_off[E], m8 = round_up(m, 8);
@@ -735,149 +765,102 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     for (int b = 0; b < 4; ++b)
         a_off[b] = (uint32_t)(g * 64 + ((b ^ ((g >> 1) & 3)) << 4) + c * 4);
 
-    // ---- one product phase over the table's items: their sums, handed to done(item, slot,
-    // sum) for PER slots an item, where sum(L, q) is value q of lane L.  A group's warps add
-    // their parts in warp order; groups wait for one another only to stage a window.
-    auto products = [&](auto &ph, auto &ld, auto per, int pitch, bool staged, auto stage, auto brow,
-                        auto done) {
-        constexpr int PER = decltype(per)::value;
-        const int grp = ph.group(), nks = 1 << ph.kshift, ks = warp & (nks - 1);
-        uint32_t st = ring_s;
-        float *part = red;  // two buffers in turn: one barrier an item
-        int buf = 0;
+    // ---- GEMM 1
+    {
+        const UpItems up(nsel, m);
+        const int n_up = up.hi > up.lo ? up.count() : 0;
+        UpPlan plan(d, NB);
+        float *sums = reinterpret_cast<float *>(region);
+        constexpr int RQ = 4 * NB;  // sums of a lane
+        const int nks = 1 << plan.kshift, ks = warp & (nks - 1);
+        uint4 xb[NB][8];
+        float inv[NB][2][2];
 #pragma unroll 1
-        for (int i0 = 0; i0 < ph.n_items; i0 += ph.groups()) {
-            const int i = i0 + grp;
-            const bool mine = i < ph.n_items;
-            const int32_t item = ph.items[mine ? i : 0];
-            float acc[NB][4];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[nb][q] = 0.f;
+        for (int base = 0; base < n_up; base += kItems) {
+            plan.n = min(kItems, n_up - base);
+            if (base > 0)
+                __syncthreads();  // the table's last use is over
+            if ((int)threadIdx.x < plan.n) {
+                int is, q, n;
+                up.get(base + threadIdx.x, is, q, n);
+                s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
+            }
+            __syncthreads();
+            UpLoader<DEPTH> ld(a, plan, s_items, ring_s);
+            uint32_t st = ring_s;
+            if (plan.n_win == 1)
+                load_slice<NB>(a, plan.column(0), xb, inv);
 #pragma unroll 1
-            for (int w = 0; w < ph.n_win; ++w) {
-                if (!staged || ph.n_win > 1) {
-                    if (i0 + w > 0)
-                        __syncthreads();  // the last window's products are done
-                    stage(w);
-                    __syncthreads();
-                    staged = true;
-                }
-                if (!mine)
-                    continue;
-                int lo, hi;
-                ph.share(w, lo, hi);
-                const int chunks = ph.chunks(w);
-                uint32_t bp[NB], ip[NB][2];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    bp[nb] = region_s + (uint32_t)(brow(item, nb * 8 + g) * pitch +
-                                                   lo * stage_cols(NB) * 2 + 16 * c);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        ip[nb][j] = smem_u32(s_inv + brow(item, nb * 8 + 2 * c + j) * chunks + lo * SC);
-                }
+            for (int b0 = 0; b0 < plan.n; b0 += plan.batch) {
+                const int b1 = min(b0 + plan.batch, plan.n);
 #pragma unroll 1
-                for (int n = hi - lo; n > 0; --n) {
-                    __syncwarp();  // the stage the loader fills next has been read
-                    ld.issue();
-                    cp_wait<DEPTH - 1>();
-                    __syncwarp();
+                for (int w = 0; w < plan.n_win; ++w) {
+                    if (plan.n_win > 1)
+                        load_slice<NB>(a, plan.column(w), xb, inv);
+#pragma unroll 1
+                    for (int i = b0 + plan.group(); i < b1; i += plan.groups()) {
+                        __syncwarp();  // the stage the loader fills next has been read
+                        ld.issue();
+                        cp_wait<DEPTH - 1>();
+                        __syncwarp();
+                        float acc[NB][4];
 #pragma unroll
-                    for (int u = 0; u < SC; ++u) {
-                        chunk_mma<NB>(acc, st + u * kChunkBytes, a_off, bp, ip, g);
+                        for (int u = 0; u < 2; ++u) {
+                            float sum[NB][4];
+                            chunk_mma<NB>(sum, st + u * kChunkBytes, a_off,
+                                          [&](int nb, int b) { return xb[nb][4 * u + b]; }, g);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const float f = inv[nb][u][q & 1];
+                                    acc[nb][q] = u == 0 ? sum[nb][q] * f : fmaf(sum[nb][q], f, acc[nb][q]);
+                                }
+                        }
+                        st = st + kStageBytes == ring_s + DEPTH * kStageBytes ? ring_s : st + kStageBytes;
+                        float *rw = sums + ((size_t)(((i - b0) << plan.kshift) + ks) * 32 + lane) * RQ;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
-                            bp[nb] += kChunkCols * 2;
-                            ip[nb][0] += 4;
-                            ip[nb][1] += 4;
+                            float4 *o = reinterpret_cast<float4 *>(rw + 4 * nb);
+                            float4 v = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
+                            if (w > 0) {
+                                const float4 p = *o;
+                                v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
+                            }
+                            *o = v;
                         }
                     }
-                    st = st + SB == ring_s + DEPTH * SB ? ring_s : st + SB;
                 }
-            }
-            if (!mine)
-                continue;
-            float *rw = part + ((size_t)(buf * kWarps + warp) * 32 + lane) * RQ;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    rw[nb * 4 + q] = acc[nb][q];
-            if (ph.kshift == 0)
-                __syncwarp();
-            else
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(32 << ph.kshift) : "memory");
-            const float *r0 = part + (size_t)(buf * kWarps + (grp << ph.kshift)) * 32 * RQ;
-#pragma unroll 1
-            for (int j = ks * 32 + lane; j < PER; j += 32 << ph.kshift)
-                done(item, j, [&](int L, int q) {
-                    const float *r = r0 + (size_t)L * RQ + q;
-                    float v = 0.f;
+                __syncthreads();
+                // the slices' sums in order, SwiGLU, h of the routed tokens
+                for (int j = threadIdx.x; j < (b1 - b0) * 64 * NB; j += kThreads) {
+                    const int32_t item = s_items[b0 + j / (64 * NB)];
+                    const int s = j & 7, tok = j % (64 * NB) >> 3;
+                    const int row = s_map[item_expert(item) * MOE_MX4_FEW_TOKENS + tok];
+                    const int nrn = up_neuron(item_first(item), s);
+                    if (s < 4 * item_quads(item) && nrn < m && row >= 0) {
+                        const float *r = sums + (((size_t)(j / (64 * NB)) << plan.kshift) * 32 + s * 4 +
+                                                 (tok & 7) / 2) * RQ + tok / 8 * 4 + (tok & 1);
+                        float gv = 0.f, uv = 0.f;
 #pragma unroll 4
-                    for (int u = 0; u < nks; ++u)
-                        v += r[(size_t)u * 32 * RQ];
-                    return v;
-                });
-            buf ^= 1;
-        }
-    };
-
-    // ---- GEMM 1
-    const UpItems up(nsel, m);
-    const int n_up = up.hi > up.lo ? up.count() : 0;
-#pragma unroll 1
-    for (int base = 0; base < n_up; base += kItems) {
-        Phase<true, NB> ph(a, s_items);
-        ph.set(min(kItems, n_up - base));
-        if (base > 0)
-            __syncthreads();  // the table's last use is over
-        if ((int)threadIdx.x < ph.n_items) {
-            int is, q, n;
-            up.get(base + threadIdx.x, is, q, n);
-            s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
-        }
-        __syncthreads();
-        Loader<true, NB, DEPTH> ld(ph, ring_s);
-        products(
-            ph, ld, std::integral_constant<int, 64 * NB>(), pitch1, one_window,
-            [&](int w) {
-                stage_rows<false>(region, pitch1, s_inv, T, w * a.win1, ph.chunks(w), d, a.x, d, 0);
-            },
-            [&](int32_t item, int tok) {
-                const int e = item_expert(item), r0 = s_off[e];
-                return s_rtok[min(r0 + tok, s_off[e + 1] - 1)];
-            },
-            [&](int32_t item, int slot, auto sum) {
-                const int e = item_expert(item), r0 = s_off[e], nr = s_off[e + 1] - r0;
-                const int s = slot & 7, tok = slot >> 3;
-                const int nrn = up_neuron(item_first(item), s);
-                const int L = s * 4 + (tok & 7) / 2, at = tok / 8 * 4 + (tok & 1);
-                if (s < 4 * item_quads(item) && nrn < m && tok < nr) {
-                    const float gv = sum(L, at), uv = sum(L, at + 2);
-                    // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
-                    a.h[(int64_t)(r0 + tok) * m8 + nrn] =
-                        __float2bfloat16_rn(__fdividef(gv, 1.0f + __expf(-gv)) * uv);
+                        for (int u = 0; u < nks; ++u) {
+                            gv += r[(size_t)u * 32 * RQ];
+                            uv += r[(size_t)u * 32 * RQ + 2];
+                        }
+                        // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
+                        a.h[(int64_t)row * m8 + nrn] =
+                            __float2bfloat16_rn(__fdividef(gv, 1.0f + __expf(-gv)) * uv);
+                    }
                 }
-            });
+                if (b1 < plan.n)
+                    __syncthreads();  // the sums are read before the next batch's are written
+            }
+        }
     }
 
     // ---- h of every CTA complete: a grid barrier; GEMM 2's first weights travel meanwhile,
     // and CTA 0 writes the routing, the tables and the statistics
-    const DownItems down(d);
-    const int n_down = nsel * down.per;
-    Phase<false, NB> ph(a, s_items);
-    auto fill_down = [&](int base) {
-        ph.set(min(kItems, n_down - base));
-        if ((int)threadIdx.x < ph.n_items) {
-            int is, q, n;
-            down.get(base + threadIdx.x, is, q, n);
-            s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
-        }
-    };
-    __syncthreads();  // h of this CTA is written, the table's last use is over
+    __syncthreads();  // h of this CTA is written
     if (threadIdx.x == kThreads - 1) {
         __threadfence();  // this CTA's h, ordered before by the barrier above
         if (atomicAdd(a.gbar, 1) == (int)gridDim.x - 1) {  // the last to arrive releases all
@@ -887,9 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             atomicAdd(a.gbar + 1, 1);
         }
     }
-    fill_down(0);
-    __syncthreads();
-    Loader<false, NB, DEPTH> ld(ph, ring_s);
+    const DownPlan plan(a, nsel);
+    DownLoader<DEPTH> ld(a, plan, s_sel, ring_s);
     if (threadIdx.x == 0) {
         const uint64_t t0 = globaltimer_ns();
         while (ld_acquire_gpu(a.gbar + 1) == gen) {
@@ -940,49 +922,104 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 
     // ---- GEMM 2 and the combine of this CTA's columns
     if (!s_abort) {
-        const int ncol = 4 * (down.hi - down.lo);
+        const int pitch = row_pitch(a.win2);
+        const uint32_t region_s = smem_u32(region);
+        uint32_t st = ring_s;
+        bool staged = false;
 #pragma unroll 1
-        for (int base = 0; base < n_down;) {
-            products(
-                ph, ld, std::integral_constant<int, 128 * NB>(), pitch2, base > 0,
-                [&](int w) {
-                    stage_rows<false>(region, pitch2, s_inv, R, w * a.win2, ph.chunks(w), m, a.h,
-                                      m8, 0);
-                },
-                [&](int32_t item, int tok) {
-                    const int e = item_expert(item);
-                    return min(s_off[e] + tok, s_off[e + 1] - 1);
-                },
-                [&](int32_t item, int slot, auto sum) {
-                    const int e = item_expert(item), r0 = s_off[e], nr = s_off[e + 1] - r0;
-                    const int s = slot & 15, tok = slot >> 4;
-                    const int L = (s & 7) * 4 + (tok & 7) / 2;
-                    const int at = tok / 8 * 4 + (tok & 1) + (s & 8) / 4;
-                    if (s < 4 * item_quads(item) && tok < nr)
-                        outs[(size_t)(r0 + tok) * ncol + 4 * (item_first(item) - down.lo) + s] =
-                            sum(L, at);
-                });
-            base += kItems;
-            if (base < n_down) {
-                __syncthreads();
-                fill_down(base);
-                __syncthreads();
-                ld.restart();
+        for (int strip = 0; strip < plan.strips; ++strip) {
+            float acc[2][NB][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[h][nb][q] = 0.f;
+#pragma unroll 1
+            for (int w = 0; w < plan.n_win; ++w) {
+                const int chunks = plan.chunks(w);
+                if (!staged || plan.n_win > 1) {
+                    if (staged)
+                        __syncthreads();  // the last window's products are done
+                    stage_rows(region, pitch, s_inv, R, w * a.win2, chunks, m, a.h, m8, s_rw);
+                    __syncthreads();
+                    staged = true;
+                }
+                DownAt at;
+                at.set(warp, chunks);
+#pragma unroll 1
+                for (; at.is < nsel; at.step(chunks)) {
+                    const int8_t *map = s_map + s_sel[at.is] * MOE_MX4_FEW_TOKENS;
+                    uint32_t bp[NB];
+                    bool on[NB];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {  // a token elsewhere: a column of zeros
+                        const int row = map[nb * 8 + g];
+                        on[nb] = row >= 0;
+                        bp[nb] = region_s + (uint32_t)(row * pitch + at.c * kChunkCols * 2 + 16 * c);
+                    }
+                    uint4 x[NB][4];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            x[nb][b] = make_uint4(0, 0, 0, 0);
+                            if (on[nb])
+                                x[nb][b] = lds128(bp[nb] + b * 64);
+                        }
+                    __syncwarp();  // the stage the loader fills next has been read
+                    ld.issue();
+                    cp_wait<DEPTH - 1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float sum[NB][4];
+                        chunk_mma<NB>(sum, st + h * kChunkBytes, a_off,
+                                      [&](int nb, int b) { return x[nb][b]; }, g);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int row = map[nb * 8 + 2 * c + j];
+                                if (row >= 0) {  // not 0 * sum: a NaN weight stays with its tokens
+                                    const float f = s_inv[row * chunks + at.c];
+                                    acc[h][nb][j] = fmaf(sum[nb][j], f, acc[h][nb][j]);
+                                    acc[h][nb][2 + j] = fmaf(sum[nb][2 + j], f, acc[h][nb][2 + j]);
+                                }
+                            }
+                    }
+                    st = st + kStageBytes == ring_s + DEPTH * kStageBytes ? ring_s : st + kStageBytes;
+                }
             }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < T * ncol; i += kThreads) {
-            const int t = i / ncol, o = i - t * ncol;
-            const int col = down_column(down.lo, o);
-            if (col >= d)
-                continue;
-            float acc = 0.f;
-            for (int j = 0; j < k; ++j) {
-                const int row = s_slot[t * k + j];
-                if (row >= 0)
-                    acc = fmaf(s_w[t * k + j], outs[(size_t)row * ncol + o], acc);
+            // the warps' sums, 8 NB floats a lane, over GEMM 2's finished rows of h
+            if (plan.n_win == 1 && strip + 1 < plan.strips)
+                staged = false;
+            __syncthreads();
+            constexpr int SQ = 8 * NB;
+            float *sums = reinterpret_cast<float *>(region);
+            float4 *o = reinterpret_cast<float4 *>(sums + ((size_t)warp * 32 + lane) * SQ);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    o[h * NB + nb] = make_float4(acc[h][nb][0], acc[h][nb][1], acc[h][nb][2], acc[h][nb][3]);
+            __syncthreads();
+            for (int j = threadIdx.x; j < kStrip * T; j += kThreads) {
+                const int s = j & (kStrip - 1), t = j / kStrip;
+                const int q = plan.lo + 8 * strip, col = down_column(q, s);
+                if (s < 4 * (plan.hi - q) && col < d) {
+                    const float *r = sums + (size_t)((s & 7) * 4 + (t & 7) / 2) * SQ +
+                                     (s >> 4) * 4 * NB + t / 8 * 4 + (s & 8) / 4 + (t & 1);
+                    float v = 0.f;
+#pragma unroll
+                    for (int u = 0; u < kWarps; ++u)
+                        v += r[(size_t)u * 32 * SQ];
+                    a.y[(int64_t)t * d + col] = __float2bfloat16_rn(v * a.scale);
+                }
             }
-            a.y[(int64_t)t * d + col] = __float2bfloat16_rn(acc * a.scale);
+            if (strip + 1 < plan.strips)
+                __syncthreads();  // the sums are read before h is staged over them
         }
     }
     cp_wait<0>();
@@ -1023,15 +1060,14 @@ static cudaError_t grid_size(int *out)
     return cudaSuccess;
 }
 
-// Columns staged at once for `rows` activation rows of K columns: all of them if they fit
-// the region and the table of scales, else as many whole chunks as do.
-static int window(int rows, int K, int nb)
+// Columns staged at once for R rows of h of K columns: all of them if they fit the region
+// and the table of scales, else as many whole chunks as do.
+static int window(int rows, int K)
 {
-    const int unit = stage_cols(nb), all = (K + unit - 1) / unit * unit;
-    int w = (kMaxRegion / rows - 64) / 2;
+    const int all = (K + kChunkCols - 1) / kChunkCols * kChunkCols;
+    int w = (kMaxRegion / rows - 64) / 2 / kChunkCols * kChunkCols;
     const int t = kMaxInv / rows * kChunkCols;
     w = w < t ? w : t;
-    w = (w < kMaxWindow ? w : kMaxWindow) / unit * unit;
     return w < all ? w : all;
 }
 
@@ -1087,23 +1123,13 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.C = p->capacity;
     a.router_type = p->router_type;
     const int R = p->T * p->k, nb = p->T <= 8 ? 1 : 2;
-    a.win1 = window(p->T, p->d, nb);
-    a.win2 = window(R, p->m, nb);
-    const int x_bytes = p->T * row_pitch(a.win1), h_bytes = R * row_pitch(a.win2);
-    a.region = round_up(x_bytes > h_bytes ? x_bytes : h_bytes, 128);
-    // two buffers of the warps' sums; the router's partial logits come there first
-    const int part = kWarps * p->T * round_up((b->Wnoise != nullptr ? 2 : 1) * p->E, 8) * 4;
-    a.red = 2 * kWarps * 32 * 4 * nb * 4;
-    a.red = round_up(a.red > part ? a.red : part, 128);
-    const int64_t quads = (p->d + 127) / 128 * 32;
-    const size_t outs = (size_t)R * 4 * ((quads + grid - 1) / grid + 1) * 4;
-    const size_t fixed = (size_t)a.region + a.red + outs, per = (size_t)kWarps * stage_bytes(nb);
+    a.win2 = window(R, p->m);
+    const int h_bytes = R * row_pitch(a.win2);
+    a.region = round_up(h_bytes > kSums ? h_bytes : kSums, 128);
     int di = 0;
-    while (di < kDepths && fixed + kDepth[di] * per > kSmemCap)
+    while (di + 1 < kDepths && (size_t)a.region + kDepth[di] * kWarps * kStageBytes > kSmemCap)
         ++di;
-    if (di == kDepths)
-        return cudaErrorInvalidValue;
-    const size_t smem = fixed + kDepth[di] * per;
+    const size_t smem = (size_t)a.region + kDepth[di] * kWarps * kStageBytes;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
