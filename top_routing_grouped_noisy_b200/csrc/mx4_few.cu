@@ -51,16 +51,16 @@ using tc::smem_u32;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kChunkCols = 128;
 constexpr int kChunkBytes = 16 * 64 + 64;     // 16 rows x 128 columns: codes, scale words
-constexpr int kStageBytes = 2 * kChunkBytes;
-constexpr int kSlice = 256;                   // GEMM 1: columns of a warp
+constexpr int kSlice = 256;                   // columns of a stage
+constexpr int kStageBytes = 4 * kChunkBytes;  // 32 rows x 256 columns: [16 rows][128 columns]
+constexpr int kRingBytes = kWarps * 2 * kStageBytes;
 constexpr int kWindow1 = kWarps * kSlice;     // columns of x at a time
 constexpr int kStrip = 32;                    // GEMM 2: output columns at a time
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
-constexpr int kSums = 64 * 1024;              // GEMM 1: the warps' sums of a batch of items
-constexpr int kMaxRegion = 96 * 1024;         // staged rows of h (or those sums)
+constexpr int kRegion = 72 * 1024;            // the warps' sums, or staged rows of h
 constexpr int kMaxInv = 1088;                 // (row, chunk) scales of a window of h
-constexpr size_t kSmemCap = 208 * 1024;       // dynamic; the static tables take 17 KB
+constexpr int kSmem = kRegion + kRingBytes;   // dynamic; the static tables take 15 KB
 
 struct Args {
     const bf16 *x, *Wg, *Wn;
@@ -73,7 +73,9 @@ struct Args {
     uint64_t wait_ns;
     float lambda, scale;
     int T, d, m, E, k, C, router_type;
-    int region, win2;  // bytes; columns of h staged at once
+    int win2;          // columns of h staged at once
+    int tk1, tk2;      // tiles of a scale tile row of W13, W2
+    int64_t w13_codes, w13_scales, w2_codes, w2_scales;  // bytes of one expert
 };
 
 // 16 or 4 bytes to shared memory; zeros where `on` is false (nothing is read then)
@@ -123,6 +125,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same with C = 0
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // pitch (bytes) of staged rows of n columns: 64 mod 128, so that the fragment loads of
 // two neighbouring rows fall into different banks
 __host__ __device__ inline int row_pitch(int n) { return (2 * n + 127) / 128 * 128 + 64; }
@@ -130,39 +142,42 @@ __host__ __device__ inline int row_pitch(int n) { return (2 * n + 127) / 128 * 1
 // --------------------------------------------------------------------- work items
 // GEMM 1 works on quads of neurons (4 that share 16 bytes of scales), 16 quads per 64
 // neurons: quad q is neurons 64 (q / 16) + q % 16 + 16 i.  A CTA takes quads [lo, hi) of
-// the selected experts' (expert-major), two per item, items inside one expert.
+// the selected experts' (expert-major), four per item, items inside one expert.
 struct UpItems {
-    int lo, hi, per, first;  // per: quads of an expert; first: items in the first expert
+    int lo, hi, per;       // per: quads of an expert (a multiple of 16)
+    int is0, at0, first;   // the first expert, the first quad in it, its items
     __device__ __forceinline__ UpItems(int nsel, int m)
     {
         per = (m + 63) / 64 * 16;
         const uint32_t all = (uint32_t)(nsel * per);  // at most 2^23, times the grid below 2^32
         lo = (int)(blockIdx.x * all / gridDim.x);
         hi = (int)((blockIdx.x + 1) * all / gridDim.x);
-        const int n0 = min(hi - lo, per - (per > 0 ? lo % per : 0));
-        first = (n0 + 1) / 2;
+        is0 = lo / per;
+        at0 = lo - is0 * per;
+        first = (min(hi - lo, per - at0) + 3) / 4;
     }
     __device__ __forceinline__ int count() const
     {
-        const int n0 = min(hi - lo, per - lo % per), rest = hi - lo - n0;
-        return first + rest / per * (per / 2) + (rest % per + 1) / 2;
+        if (hi <= lo)
+            return 0;
+        const int rest = hi - lo - min(hi - lo, per - at0);
+        return first + rest / per * (per / 4) + (rest % per + 3) / 4;
     }
-    // item i: its expert (position among the selected), first quad, quads (1 or 2)
+    // item i: its expert (position among the selected), first quad, quads (1..4)
     __device__ __forceinline__ void get(int i, int &is, int &q, int &n) const
     {
-        int at;  // quad index over all experts
-        if (i < first) {
-            at = lo + 2 * i;
-        } else {
-            const int j = i - first;
-            at = (lo / per + 1 + j / (per / 2)) * per + 2 * (j % (per / 2));
+        is = is0;
+        q = at0 + 4 * i;
+        if (i >= first) {
+            i -= first;
+            for (++is; i >= per / 4; ++is)
+                i -= per / 4;
+            q = 4 * i;
         }
-        is = at / per;
-        q = at - is * per;
-        n = min(2, min(hi - at, per - q));
+        n = min(4, min(hi - is * per - q, per - q));
     }
 };
-// neuron s (0..7) of an item that starts at quad q
+// neuron s (0..15) of an item that starts at quad q
 __device__ __forceinline__ int up_neuron(int q, int s)
 {
     const int qq = q + s / 4;
@@ -187,23 +202,17 @@ __device__ __forceinline__ int item_expert(int32_t v) { return v & 31; }
 __device__ __forceinline__ int item_quads(int32_t v) { return v >> 5 & 7; }
 __device__ __forceinline__ int item_first(int32_t v) { return v >> 8; }
 
-// Scale word of row r, chunk c: its place in an expert's scales
-__device__ __forceinline__ int64_t word_at(int r, int c, int tk)
-{
-    return ((int64_t)(r >> 7) * tk + c) * kMx4Tile + (r & 31) * 16 + (r >> 5 & 3) * 4;
-}
-
 // How GEMM 1 is shared out: 2^kshift warps (a group) hold the slices of a window of x, the
 // groups take the items of a batch in turn.
 struct UpPlan {
-    int n, batch, kshift, n_win;  // items in the table; of a batch; ; windows
+    int n, batch, kshift, n_win;  // n: items in the table; batch: items between reductions
     __device__ __forceinline__ UpPlan(int d, int nb)
     {
         n = 0;
         n_win = (d + kWindow1 - 1) / kWindow1;
         const int slices = (min(d, kWindow1) + kSlice - 1) / kSlice;
         kshift = 32 - __clz(slices - 1);  // 0 for one slice
-        batch = kSums / (nb * 512) >> kshift;
+        batch = kRegion / (nb * 1024) >> kshift;
     }
     __device__ __forceinline__ int group() const { return (int)(threadIdx.x >> 5) >> kshift; }
     __device__ __forceinline__ int groups() const { return kWarps >> kshift; }
@@ -213,190 +222,169 @@ struct UpPlan {
         return w * kWindow1 + ((int)(threadIdx.x >> 5) & ((1 << kshift) - 1)) * kSlice;
     }
 };
-
-// Loader of GEMM 1, one warp's: a stage is 16 rows (an item) x the 256 columns of the warp's
-// slice; order: batches of items, windows, the group's items.
-template <int DEPTH>
-struct UpLoader {
-    const Args &a;
-    const UpPlan &p;
-    const int32_t *items;
-    uint32_t ring, st, dst;
-    int b0, w, i;
-    __device__ __forceinline__ UpLoader(const Args &args, const UpPlan &plan, const int32_t *table,
-                                        uint32_t r)
-        : a(args), p(plan), items(table), ring(r), st(r), b0(0), w(0), i(plan.group())
+// A warp's way through a table: batches of items, windows, the group's items.
+struct UpWalk {
+    int b0, w, i, end;  // end: of the batch
+    __device__ __forceinline__ UpWalk(const UpPlan &p) : b0(0), w(0), i(p.group()), end(min(p.batch, p.n))
     {
-        const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
-        dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-        skip();
-#pragma unroll 1
-        for (int n = 0; n < DEPTH - 1; ++n)
-            issue();
+        skip(p);
     }
-    // past the ends of batches and windows, to an item of this group or to the end
-    __device__ __forceinline__ void skip()
+    __device__ __forceinline__ bool on(const UpPlan &p) const { return b0 < p.n; }
+    __device__ __forceinline__ void next(const UpPlan &p)
     {
-        while (b0 < p.n && i >= min(b0 + p.batch, p.n)) {
+        i += p.groups();
+        skip(p);
+    }
+    __device__ __forceinline__ void skip(const UpPlan &p)
+    {
+        while (__builtin_expect(i >= end && b0 < p.n, 0)) {
             if (++w == p.n_win) {
                 w = 0;
-                b0 += p.batch;
+                b0 = end;
+                end = min(b0 + p.batch, p.n);
             }
             i = b0 + p.group();
         }
     }
-    // row of the expert's W13 that A row r of an item holds; -1: none
-    __device__ __forceinline__ int row(int32_t item, int r) const
-    {
-        const int s = r & 7, nr = up_neuron(item_first(item), s);
-        return (s < 4 * item_quads(item) && nr < a.m) ? (nr >> 4) * 32 + (nr & 15) + (r >= 8 ? 16 : 0)
-                                                       : -1;
-    }
-    __device__ __forceinline__ void issue()
-    {
-        if (b0 < p.n) {
-            const int lane = threadIdx.x & 31;
-            const int32_t item = items[i];
-            const int rows = 2 * round_up(a.m, 16), tk = (a.d + 127) >> 7, col = p.column(w);
-            const uint8_t *ce = a.W13q + (int64_t)(item_expert(item) * rows) * (a.d / 2);
-            const uint8_t *se = a.W13s + (int64_t)(item_expert(item) * ((rows + 127) >> 7)) * tk * kMx4Tile;
-            const int r0 = row(item, lane >> 2), r1 = row(item, (lane >> 2) + 8);
-            const int at = col / 2 + (lane & 3) * 16;  // columns past d are zeros
-            const uint8_t *s0 = ce + (int64_t)max(r0, 0) * (a.d / 2) + at;
-            const uint8_t *s1 = ce + (int64_t)max(r1, 0) * (a.d / 2) + at;
-            const bool in0 = at < a.d / 2, in1 = at + 64 < a.d / 2;
-            cp16(st + dst, s0, in0 && r0 >= 0);
-            cp16(st + dst + 512, s1, in0 && r1 >= 0);
-            cp16(st + kChunkBytes + dst, in1 ? s0 + 64 : s0, in1 && r0 >= 0);
-            cp16(st + kChunkBytes + dst + 512, in1 ? s1 + 64 : s1, in1 && r1 >= 0);
-            // lanes 0..15: the words of the first chunk; 16..31: of the second
-            const int rs = row(item, lane & 15), ch = (col >> 7) + (lane >> 4);
-            const bool ins = rs >= 0 && ch < tk;
-            cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4,
-                se + (ins ? word_at(rs, ch, tk) : 0), ins);
-            i += p.groups();
-            skip();
-        }
-        cp_commit();
-        st = st + kStageBytes == ring + DEPTH * kStageBytes ? ring : st + kStageBytes;
-    }
 };
 
-// How GEMM 2 is shared out: the (selected expert, chunk) pairs of a window of h go round the
-// warps.
+// A lane's place in a stage: row (lane / 4) of a 16-row chunk, 16-byte piece lane % 4
+__device__ __forceinline__ uint32_t stage_place()
+{
+    const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
+    return (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+
+// Fills a stage of GEMM 1 (one group of copies): the item's 16 neurons, W1 rows of the first 8
+// and their W3 rows, then the other 8, x the 256 columns from col on.  Neuron s of an item
+// that starts at quad q lies at W13 row 128 (qq / 16) + 32 (s % 4) + qq % 16 with qq = q +
+// s / 4, its W3 row 16 further; the scale words at 16 (qq % 16 [+ 16]) + 4 (s % 4) of tile
+// qq / 16.  Rows past the expert's and columns past d become zeros.
+__device__ __forceinline__ void up_fill(const Args &a, int32_t item, int col, uint32_t st)
+{
+    const int lane = threadIdx.x & 31;
+    const int e = item_expert(item), n4 = 4 * item_quads(item), q = item_first(item);
+    const int half = a.d >> 1, at = (col >> 1) + (lane & 3) * 16;
+    const uint8_t *ce = a.W13q + e * a.w13_codes + at;
+    const bool in0 = at < half, in1 = at + 64 < half;
+    st += stage_place();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int s = 8 * h + (lane >> 2), qq = q + (s >> 2), t = (qq >> 4) * 64 + (qq & 15);
+        const bool on = s < n4 && t + 16 * (s & 3) < a.m;
+        const uint8_t *s0 = ce + (int64_t)((qq >> 4) * 128 + 32 * (s & 3) + (qq & 15)) * half;
+        const uint8_t *s1 = s0 + 16 * half;
+        cp16(st + 2 * h * kChunkBytes, s0, on && in0);
+        cp16(st + 2 * h * kChunkBytes + 512, s1, on && in0);
+        cp16(st + (2 * h + 1) * kChunkBytes, s0 + 64, on && in1);
+        cp16(st + (2 * h + 1) * kChunkBytes + 512, s1 + 64, on && in1);
+    }
+    // scale words: lane % 16 the row of the chunk, lane / 16 the chunk
+    const int ch = (col >> 7) + (lane >> 4);
+    const uint8_t *se = a.W13s + e * a.w13_scales + (lane & 8) * 32 + (int64_t)ch * kMx4Tile;
+    st += (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4 - stage_place();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int s = 8 * h + (lane & 7), qq = q + (s >> 2);
+        const bool on = s < n4 && (qq >> 4) * 64 + (qq & 15) + 16 * (s & 3) < a.m && ch < a.tk1;
+        cp4(st + 2 * h * kChunkBytes,
+            se + (int64_t)((qq >> 4) * a.tk1) * kMx4Tile + (qq & 15) * 16 + (s & 3) * 4, on);
+    }
+    cp_commit();
+}
+
+// How GEMM 2 is shared out: the (selected expert, 256 columns of h) pairs of a window go
+// round the warps.
 struct DownPlan {
-    int lo, hi, strips, nsel, K32, tk, win, n_win;
+    int lo, hi, strips, nsel, half, win, n_win;  // win: columns
     __device__ __forceinline__ DownPlan(const Args &a, int sel)
     {
         const uint32_t all = (uint32_t)((a.d + 127) / 128 * 32);
         lo = (int)(blockIdx.x * all / gridDim.x);
         hi = (int)((blockIdx.x + 1) * all / gridDim.x);
-        strips = (4 * (hi - lo) + kStrip - 1) / kStrip;
+        strips = sel == 0 ? 0 : (4 * (hi - lo) + kStrip - 1) / kStrip;
         nsel = sel;
-        K32 = mx4_k32(a.m);
-        tk = (K32 + 127) >> 7;
-        win = a.win2 >> 7;  // in chunks
-        n_win = (tk + win - 1) / win;
+        half = mx4_k32(a.m) >> 1;
+        win = a.win2;
+        n_win = (2 * half + win - 1) / win;
     }
-    __device__ __forceinline__ int chunks(int w) const { return min(win, tk - w * win); }
+    __device__ __forceinline__ int units(int w) const
+    {
+        return (min(win, 2 * half - w * win) + kSlice - 1) / kSlice;
+    }
 };
-// the warp's place in the pairs of a window: expert is (among the selected), chunk c
-struct DownAt {
-    int is, c;
-    __device__ __forceinline__ void set(int n, int chunks)
+// A warp's way: strips, windows, its pairs (is: expert among the selected, u: unit).
+struct DownWalk {
+    int strip, w, n, is, u;
+    __device__ __forceinline__ DownWalk(const DownPlan &p) : strip(0), w(0) { open(p); }
+    __device__ __forceinline__ bool on(const DownPlan &p) const { return strip < p.strips; }
+    __device__ __forceinline__ void open(const DownPlan &p)
     {
-        is = n / chunks;
-        c = n - is * chunks;
+        while (strip < p.strips) {
+            n = p.units(w);
+            is = 0;
+            u = (int)threadIdx.x >> 5;
+            wrap();
+            if (is < p.nsel)
+                return;
+            leave(p);
+        }
     }
-    __device__ __forceinline__ void step(int chunks)
+    __device__ __forceinline__ void wrap()
     {
-        c += kWarps;
-        while (c >= chunks) {
-            c -= chunks;
+        while (u >= n) {
+            u -= n;
             ++is;
+        }
+    }
+    __device__ __forceinline__ void leave(const DownPlan &p)
+    {
+        if (++w == p.n_win) {
+            w = 0;
+            ++strip;
+        }
+    }
+    __device__ __forceinline__ void next(const DownPlan &p)
+    {
+        u += kWarps;
+        wrap();
+        if (__builtin_expect(is >= p.nsel, 0)) {
+            leave(p);
+            open(p);
         }
     }
 };
 
-// Loader of GEMM 2, one warp's: a stage is the strip's 32 rows x one chunk; order: strips,
-// windows, the warp's pairs.
-template <int DEPTH>
-struct DownLoader {
-    const Args &a;
-    const DownPlan &p;
-    const int32_t *sel;
-    uint32_t ring, st, dst;
-    int strip, w;
-    DownAt at;
-    int64_t off[4], soff;  // this lane's pieces of rows (lane / 4) + 8 i, its scale word
-    bool on[4], ons;
-    __device__ __forceinline__ DownLoader(const Args &args, const DownPlan &plan,
-                                          const int32_t *selected, uint32_t r)
-        : a(args), p(plan), sel(selected), ring(r), st(r), strip(0), w(0)
-    {
-        const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
-        dst = (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-        open();
-        at.set((int)threadIdx.x >> 5, p.chunks(0));
-        skip();
-#pragma unroll 1
-        for (int n = 0; n < DEPTH - 1; ++n)
-            issue();
-    }
-    __device__ __forceinline__ int column(int r) const
-    {
-        const int q = p.lo + 8 * strip, col = down_column(q, r);
-        return r < 4 * (p.hi - q) && col < a.d ? col : -1;
-    }
-    // the rows of a strip
-    __device__ __forceinline__ void open()
-    {
-        const int lane = threadIdx.x & 31;
+// Fills a stage of GEMM 2 (one group of copies): the strip's 32 rows of expert e's W2 x the
+// 256 columns from col on; rows past the strip and columns past K32 become zeros.
+__device__ __forceinline__ void down_fill(const Args &a, const DownPlan &p, int strip, int e, int col,
+                                          uint32_t st)
+{
+    const int lane = threadIdx.x & 31, q = p.lo + 8 * strip, rows = 4 * (p.hi - q);
+    const int at = (col >> 1) + (lane & 3) * 16;
+    const uint8_t *ce = a.W2q + e * a.w2_codes + at;
+    const bool in0 = at < p.half, in1 = at + 64 < p.half;
+    st += stage_place();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int col = column((lane >> 2) + 8 * i);
-            on[i] = col >= 0;
-            off[i] = (int64_t)max(col, 0) * (p.K32 / 2) + (lane & 3) * 16;
-        }
-        const int col = column(lane);
-        ons = col >= 0;
-        soff = word_at(max(col, 0), 0, p.tk);
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 2) + 8 * i, row = down_column(q, r);
+        const bool on = r < rows && row < a.d;
+        const uint8_t *s0 = ce + (int64_t)row * p.half;
+        cp16(st + (i >> 1) * 2 * kChunkBytes + (i & 1) * 512, s0, on && in0);
+        cp16(st + ((i >> 1) * 2 + 1) * kChunkBytes + (i & 1) * 512, s0 + 64, on && in1);
     }
-    // past the ends of windows and strips
-    __device__ __forceinline__ void skip()
-    {
-        while (strip < p.strips && at.is >= p.nsel) {
-            if (++w == p.n_win) {
-                w = 0;
-                if (++strip < p.strips)
-                    open();
-            }
-            at.set((int)threadIdx.x >> 5, p.chunks(w));
-            if (p.nsel == 0)
-                strip = p.strips;
-        }
-    }
-    __device__ __forceinline__ void issue()
-    {
-        if (strip < p.strips) {
-            const int lane = threadIdx.x & 31, e = sel[at.is], c = w * p.win + at.c;
-            const uint8_t *ce = a.W2q + (int64_t)e * a.d * (p.K32 / 2) + c * 64;
-            const bool in = c * 64 + (lane & 3) * 16 < p.K32 / 2;  // columns past K32 are zeros
+    const int ch = (col >> 7) + (lane >> 4);
+    const uint8_t *se = a.W2s + e * a.w2_scales + (int64_t)ch * kMx4Tile;
+    st += (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4 - stage_place();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool ok = in && on[i];
-                cp16(st + (i >> 1) * kChunkBytes + (i & 1) * 512 + dst, ok ? ce + off[i] : a.W2q, ok);
-            }
-            const uint8_t *se = a.W2s + (int64_t)(e * ((a.d + 127) >> 7)) * p.tk * kMx4Tile;
-            cp4(st + (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4, se + soff + (int64_t)c * kMx4Tile,
-                ons);
-            at.step(p.chunks(w));
-            skip();
-        }
-        cp_commit();
-        st = st + kStageBytes == ring + DEPTH * kStageBytes ? ring : st + kStageBytes;
+    for (int h = 0; h < 2; ++h) {
+        const int r = 16 * h + (lane & 15), row = down_column(q, r);
+        cp4(st + 2 * h * kChunkBytes,
+            se + (int64_t)((row >> 7) * a.tk2) * kMx4Tile + (row & 31) * 16 + (row >> 5 & 3) * 4,
+            r < rows && row < a.d && ch < a.tk2);
     }
-};
+    cp_commit();
+}
 
 // --------------------------------------------------------------------- activations
 // The power of two that takes a maximum with the bf16 magnitude bits `top` into [2^13, 2^14):
@@ -537,11 +525,6 @@ __device__ __forceinline__ void chunk_mma(float (&sum)[NB][4], uint32_t st, cons
     word_scales(lds32(st + 1024 + g * 4), s0);
     word_scales(lds32(st + 1056 + g * 4), s1);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            sum[nb][q] = 0.f;
-#pragma unroll
     for (int b = 0; b < 4; ++b) {
         uint32_t a0[4], a1[4];
         mx4_halves8(lds32(st + off[b]), a0);
@@ -549,13 +532,14 @@ __device__ __forceinline__ void chunk_mma(float (&sum)[NB][4], uint32_t st, cons
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const uint4 v = x(nb, b);
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(t, a0[0], a1[0], a0[1], a1[1], v.x, v.y);
+            float t[4];
+            mma_f16_first(t, a0[0], a1[0], a0[1], a1[1], v.x, v.y);
             mma_f16(t, a0[2], a1[2], a0[3], a1[3], v.z, v.w);
-            sum[nb][0] = fmaf(t[0], s0[b], sum[nb][0]);
-            sum[nb][1] = fmaf(t[1], s0[b], sum[nb][1]);
-            sum[nb][2] = fmaf(t[2], s1[b], sum[nb][2]);
-            sum[nb][3] = fmaf(t[3], s1[b], sum[nb][3]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float f = q < 2 ? s0[b] : s1[b];
+                sum[nb][q] = b == 0 ? t[q] * f : fmaf(t[q], f, sum[nb][q]);
+            }
         }
     }
 }
@@ -654,23 +638,24 @@ __device__ __noinline__ void router_logits(const Args &a, char *stage, int stage
 }
 
 // --------------------------------------------------------------------- the kernel
-template <int NB, int DEPTH>
+template <int NB>
 __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_constant__ Args a)
 {
     extern __shared__ __align__(128) char sm[];
-    __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE], s_cnt[kMaxE], s_kept[kMaxE];
+    __shared__ uint32_t s_mask[kMaxE];  // tokens that chose an expert
+    __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE];
     __shared__ int32_t s_idx[kMaxRows], s_slot[kMaxRows], s_rtok[kMaxRows];
     __shared__ int8_t s_map[kMaxE * MOE_MX4_FEW_TOKENS];  // row of (expert, token), -1 none
     __shared__ float s_w[kMaxRows], s_rw[kMaxRows], s_inv[kMaxInv];
     __shared__ float s_lg[MOE_MX4_FEW_TOKENS * 32], s_prob[MOE_MX4_FEW_TOKENS * kMaxE],
         s_gw[MOE_MX4_FEW_TOKENS * kMaxE];
     __shared__ int32_t s_items[kItems];
-    __shared__ int s_nsel, s_abort;
+    __shared__ int s_abort;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int T = a.T, E = a.E, k = a.k, d = a.d, m = a.m;
     char *region = sm;  // the router's sums, GEMM 1's, then the rows of h
-    char *my_ring = sm + a.region + warp * DEPTH * kStageBytes;
+    char *my_ring = sm + kRegion + warp * 2 * kStageBytes;
     const uint32_t ring_s = smem_u32(my_ring);
     // the grid barrier's generation before this launch's barrier (it changes only once
     // every CTA has arrived, this one included)
@@ -679,49 +664,35 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         s_abort = 0;
         gen = ld_acquire_gpu(a.gbar + 1);
     }
-    for (int i = threadIdx.x; i < E * MOE_MX4_FEW_TOKENS; i += kThreads)
-        s_map[i] = -1;
+    s_map[threadIdx.x] = -1;
+    if (threadIdx.x < kMaxE)
+        s_mask[threadIdx.x] = 0;
 
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
     float *part = reinterpret_cast<float *>(region);
     switch ((nout + 7) / 8) {
-    case 1: router_logits<1>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
-    case 2: router_logits<2>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
-    case 3: router_logits<3>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
-    default: router_logits<4>(a, my_ring, DEPTH * kStageBytes, part, s_lg); break;
+    case 1: router_logits<1>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
+    case 2: router_logits<2>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
+    case 3: router_logits<3>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
+    default: router_logits<4>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
     }
     if (warp < T)
         gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
                         a.noise + (a.noise != nullptr ? (size_t)warp * E : 0), a.bias, a.router_type,
                         s_idx + warp * k, s_w + warp * k, s_prob + warp * E, s_gw + warp * E,
                         a.status);
+    __syncwarp();
+    if (warp < T && lane < k && s_idx[warp * k + lane] >= 0)
+        atomicOr(&s_mask[s_idx[warp * k + lane]], 1u << warp);
     __syncthreads();
-    // ---- dispatch tables by warp 0 (lane e: expert e): stable by token, assignments past the
-    // capacity dropped
-    if (warp == 0) {
-        constexpr int B = kMaxRows / 32;
-        const int n = T * k;
-        int v[B], rank[B], cnt = 0;
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            v[b] = 32 * b + lane < n ? s_idx[32 * b + lane] : -1;
-            rank[b] = 0;
-        }
-        for (int e = 0; e < E; ++e) {
-            int base = 0;
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                if (32 * b >= n)
-                    break;
-                const uint32_t hit = __ballot_sync(0xffffffffu, v[b] == e);
-                if (v[b] == e)
-                    rank[b] = base + __popc(hit & ((1u << lane) - 1));
-                base += __popc(hit);
-            }
-            cnt = lane == e ? base : cnt;
-        }
-        const int kept = a.C < 0 ? cnt : min(cnt, a.C);
+    // ---- dispatch tables (stable by token, assignments past the capacity dropped).  s_mask[e]
+    // has a bit for each token that chose expert e, so a row's rank is a population count and
+    // every warp makes the experts' tables for itself (all write the same values).
+    int nsel;
+    {
+        const uint32_t chosen = lane < E ? s_mask[lane] : 0u;
+        const int cnt = __popc(chosen), kept = a.C < 0 ? cnt : min(cnt, a.C);
         int off = kept;  // inclusive prefix sum
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -729,37 +700,31 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             off += lane >= o ? u : 0;
         }
         const uint32_t used = __ballot_sync(0xffffffffu, kept > 0);
+        nsel = __popc(used);
         if (lane < E) {
-            s_cnt[lane] = cnt;
-            s_kept[lane] = kept;
             s_off[lane + 1] = off;
+            if (lane == 0)
+                s_off[0] = 0;
             if (kept > 0)
                 s_sel[__popc(used & ((1u << lane) - 1))] = lane;
         }
-        if (lane == 0) {
-            s_off[0] = 0;
-            s_nsel = __popc(used);
-        }
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            if (32 * b >= n)
-                break;
-            const int e = max(v[b], 0), i = 32 * b + lane;
-            const int first = __shfl_sync(0xffffffffu, off - kept, e);
-            const int room = __shfl_sync(0xffffffffu, kept, e);
-            const int row = v[b] >= 0 && rank[b] < room ? first + rank[b] : -1;
-            if (i < n)
-                s_slot[i] = row;
+        // warp t: the rows of token t
+        const int e = warp < T && lane < k ? s_idx[warp * k + lane] : -1;
+        const int first = __shfl_sync(0xffffffffu, off - kept, max(e, 0));
+        const int room = __shfl_sync(0xffffffffu, kept, max(e, 0));
+        if (warp < T && lane < k) {
+            const int rank = e < 0 ? 0 : __popc(s_mask[e] & ((1u << warp) - 1));
+            const int row = e >= 0 && rank < room ? first + rank : -1;
+            s_slot[warp * k + lane] = row;
             if (row >= 0) {
-                const int t = i / k;
-                s_rtok[row] = t;
-                s_rw[row] = s_w[i];
-                s_map[e * MOE_MX4_FEW_TOKENS + t] = (int8_t)row;
+                s_rtok[row] = warp;
+                s_rw[row] = s_w[warp * k + lane];
+                s_map[e * MOE_MX4_FEW_TOKENS + warp] = (int8_t)row;
             }
         }
+        __syncwarp();
     }
-    __syncthreads();
-    const int nsel = s_nsel, R = s_off[E], m8 = round_up(m, 8);
+    const int R = s_off[E], m8 = round_up(m, 8);
     uint32_t a_off[4];  // this lane's words of A row g in a chunk
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -768,10 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // ---- GEMM 1
     {
         const UpItems up(nsel, m);
-        const int n_up = up.hi > up.lo ? up.count() : 0;
+        const int n_up = up.count();
         UpPlan plan(d, NB);
         float *sums = reinterpret_cast<float *>(region);
-        constexpr int RQ = 4 * NB;  // sums of a lane
+        // sums of an item: [slice][half][nb][lane] float4
         const int nks = 1 << plan.kshift, ks = warp & (nks - 1);
         uint4 xb[NB][8];
         float inv[NB][2][2];
@@ -780,14 +745,18 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             plan.n = min(kItems, n_up - base);
             if (base > 0)
                 __syncthreads();  // the table's last use is over
-            if ((int)threadIdx.x < plan.n) {
+            for (int j = lane; j < plan.n; j += 32) {  // every warp for itself, the same values
                 int is, q, n;
-                up.get(base + threadIdx.x, is, q, n);
-                s_items[threadIdx.x] = item_pack(s_sel[is], q, n);
+                up.get(base + j, is, q, n);
+                s_items[j] = item_pack(s_sel[is], q, n);
             }
-            __syncthreads();
-            UpLoader<DEPTH> ld(a, plan, s_items, ring_s);
-            uint32_t st = ring_s;
+            __syncwarp();
+            UpWalk ld(plan);
+            if (ld.on(plan)) {
+                up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s);
+                ld.next(plan);
+            }
+            uint32_t st = 0;
             if (plan.n_win == 1)
                 load_slice<NB>(a, plan.column(0), xb, inv);
 #pragma unroll 1
@@ -799,57 +768,72 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                         load_slice<NB>(a, plan.column(w), xb, inv);
 #pragma unroll 1
                     for (int i = b0 + plan.group(); i < b1; i += plan.groups()) {
-                        __syncwarp();  // the stage the loader fills next has been read
-                        ld.issue();
-                        cp_wait<DEPTH - 1>();
+                        __syncwarp();  // the other stage has been read
+                        if (ld.on(plan)) {
+                            up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s + (st ^ kStageBytes));
+                            ld.next(plan);
+                        } else {
+                            cp_commit();
+                        }
+                        cp_wait<1>();
                         __syncwarp();
-                        float acc[NB][4];
+                        float4 *o = reinterpret_cast<float4 *>(sums) +
+                                    (size_t)((((i - b0) << plan.kshift) + ks) * 2 * NB) * 32 + lane;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            float acc[NB][4];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            float sum[NB][4];
-                            chunk_mma<NB>(sum, st + u * kChunkBytes, a_off,
-                                          [&](int nb, int b) { return xb[nb][4 * u + b]; }, g);
+                            for (int u = 0; u < 2; ++u) {
+                                float sum[NB][4];
+                                chunk_mma<NB>(sum, ring_s + st + (2 * h + u) * kChunkBytes, a_off,
+                                              [&](int nb, int b) { return xb[nb][4 * u + b]; }, g);
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
+                                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const float f = inv[nb][u][q & 1];
-                                    acc[nb][q] = u == 0 ? sum[nb][q] * f : fmaf(sum[nb][q], f, acc[nb][q]);
-                                }
-                        }
-                        st = st + kStageBytes == ring_s + DEPTH * kStageBytes ? ring_s : st + kStageBytes;
-                        float *rw = sums + ((size_t)(((i - b0) << plan.kshift) + ks) * 32 + lane) * RQ;
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            float4 *o = reinterpret_cast<float4 *>(rw + 4 * nb);
-                            float4 v = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
-                            if (w > 0) {
-                                const float4 p = *o;
-                                v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
+                                    for (int q = 0; q < 4; ++q) {
+                                        const float f = inv[nb][u][q & 1];
+                                        acc[nb][q] = u == 0 ? sum[nb][q] * f : fmaf(sum[nb][q], f, acc[nb][q]);
+                                    }
                             }
-                            *o = v;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                float4 v = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
+                                if (w > 0) {
+                                    const float4 p = o[nb * 32];
+                                    v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
+                                }
+                                o[nb * 32] = v;
+                            }
+                            o += NB * 32;
                         }
+                        st ^= kStageBytes;
                     }
                 }
                 __syncthreads();
-                // the slices' sums in order, SwiGLU, h of the routed tokens
-                for (int j = threadIdx.x; j < (b1 - b0) * 64 * NB; j += kThreads) {
-                    const int32_t item = s_items[b0 + j / (64 * NB)];
-                    const int s = j & 7, tok = j % (64 * NB) >> 3;
-                    const int row = s_map[item_expert(item) * MOE_MX4_FEW_TOKENS + tok];
-                    const int nrn = up_neuron(item_first(item), s);
-                    if (s < 4 * item_quads(item) && nrn < m && row >= 0) {
-                        const float *r = sums + (((size_t)(j / (64 * NB)) << plan.kshift) * 32 + s * 4 +
-                                                 (tok & 7) / 2) * RQ + tok / 8 * 4 + (tok & 1);
-                        float gv = 0.f, uv = 0.f;
+                // the slices' sums in order, SwiGLU, h of the routed tokens: one warp per item,
+                // half and nb; lane (s, c) has gate and up of neuron s for tokens 2c, 2c + 1
+#pragma unroll 1
+                for (int j = warp; j < (b1 - b0) * 2 * NB; j += kWarps) {
+                    const int i = j / (2 * NB), hb = j % (2 * NB);
+                    const int32_t item = s_items[b0 + i];
+                    const float4 *r = reinterpret_cast<const float4 *>(sums) +
+                                      (size_t)((i << plan.kshift) * 2 * NB + hb) * 32 + lane;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-                        for (int u = 0; u < nks; ++u) {
-                            gv += r[(size_t)u * 32 * RQ];
-                            uv += r[(size_t)u * 32 * RQ + 2];
-                        }
+                    for (int u = 0; u < nks; ++u) {
+                        const float4 p = r[(size_t)u * 64 * NB];
+                        v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+                    }
+                    const int s = hb / NB * 8 + g, nrn = up_neuron(item_first(item), s);
+                    const int8_t *map = s_map + item_expert(item) * MOE_MX4_FEW_TOKENS + hb % NB * 8 + 2 * c;
+                    if (s < 4 * item_quads(item) && nrn < m) {
                         // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
-                        a.h[(int64_t)row * m8 + nrn] =
-                            __float2bfloat16_rn(__fdividef(gv, 1.0f + __expf(-gv)) * uv);
+                        if (map[0] >= 0)
+                            a.h[(int64_t)map[0] * m8 + nrn] =
+                                __float2bfloat16_rn(__fdividef(v.x, 1.0f + __expf(-v.x)) * v.z);
+                        if (map[1] >= 0)
+                            a.h[(int64_t)map[1] * m8 + nrn] =
+                                __float2bfloat16_rn(__fdividef(v.y, 1.0f + __expf(-v.y)) * v.w);
                     }
                 }
                 if (b1 < plan.n)
@@ -871,7 +855,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         }
     }
     const DownPlan plan(a, nsel);
-    DownLoader<DEPTH> ld(a, plan, s_sel, ring_s);
+    DownWalk ld(plan);
+    if (ld.on(plan)) {
+        down_fill(a, plan, ld.strip, s_sel[ld.is], ld.w * plan.win + ld.u * kSlice, ring_s);
+        ld.next(plan);
+    }
     if (threadIdx.x == 0) {
         const uint64_t t0 = globaltimer_ns();
         while (ld_acquire_gpu(a.gbar + 1) == gen) {
@@ -900,11 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 sp += s_prob[t * E + t1];
                 sg += s_gw[t * E + t1];
             }
-            a.counts[t1] = s_cnt[t1];
-            a.kept[t1] = s_kept[t1];
+            const int cnt = __popc(s_mask[t1]);
+            a.counts[t1] = cnt;
+            a.kept[t1] = s_off[t1 + 1] - s_off[t1];
             a.probs_sum[t1] = sp;
             a.importance[t1] = sg;
-            a.f[t1] = (float)((double)s_cnt[t1] / ((double)T * k));
+            a.f[t1] = (float)((double)cnt / ((double)T * k));
             a.P[t1] = (float)((double)sp / (double)T);
         }
         if (t1 == nt - 1) {
@@ -913,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 float sp = 0.f;
                 for (int t = 0; t < T; ++t)
                     sp += s_prob[t * E + e];
-                sfp += ((double)s_cnt[e] / ((double)T * k)) * ((double)sp / (double)T);
+                sfp += ((double)__popc(s_mask[e]) / ((double)T * k)) * ((double)sp / (double)T);
             }
             a.loss[0] = (float)(a.lambda * sfp);
         }
@@ -922,12 +911,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 
     // ---- GEMM 2 and the combine of this CTA's columns
     if (!s_abort) {
-        const int pitch = row_pitch(a.win2);
+        const int pitch = row_pitch(a.win2), strips = (4 * (plan.hi - plan.lo) + kStrip - 1) / kStrip;
         const uint32_t region_s = smem_u32(region);
-        uint32_t st = ring_s;
-        bool staged = false;
+        uint32_t st = 0;
 #pragma unroll 1
-        for (int strip = 0; strip < plan.strips; ++strip) {
+        for (int strip = 0; strip < strips; ++strip) {
             float acc[2][NB][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -938,101 +926,109 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                         acc[h][nb][q] = 0.f;
 #pragma unroll 1
             for (int w = 0; w < plan.n_win; ++w) {
-                const int chunks = plan.chunks(w);
-                if (!staged || plan.n_win > 1) {
-                    if (staged)
-                        __syncthreads();  // the last window's products are done
-                    stage_rows(region, pitch, s_inv, R, w * a.win2, chunks, m, a.h, m8, s_rw);
-                    __syncthreads();
-                    staged = true;
-                }
-                DownAt at;
-                at.set(warp, chunks);
+                const int units = plan.units(w), chunks = 2 * units;
+                if (strip + w > 0)
+                    __syncthreads();  // the region's last use is over
+                stage_rows(region, pitch, s_inv, R, w * a.win2, chunks, m, a.h, m8, s_rw);
+                __syncthreads();
+                int is = 0, u = warp;
 #pragma unroll 1
-                for (; at.is < nsel; at.step(chunks)) {
-                    const int8_t *map = s_map + s_sel[at.is] * MOE_MX4_FEW_TOKENS;
-                    uint32_t bp[NB];
-                    bool on[NB];
+                while (true) {
+                    while (u >= units) {
+                        u -= units;
+                        ++is;
+                    }
+                    if (is >= nsel)
+                        break;
+                    const int8_t *map = s_map + s_sel[is] * MOE_MX4_FEW_TOKENS;
+                    uint4 x[NB][8];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {  // a token elsewhere: a column of zeros
                         const int row = map[nb * 8 + g];
-                        on[nb] = row >= 0;
-                        bp[nb] = region_s + (uint32_t)(row * pitch + at.c * kChunkCols * 2 + 16 * c);
+                        const uint32_t bp = region_s + (uint32_t)(row * pitch + u * kSlice * 2 + 16 * c);
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            x[nb][b] = make_uint4(0, 0, 0, 0);
+                            if (row >= 0)
+                                x[nb][b] = lds128(bp + b * 64);
+                        }
                     }
-                    uint4 x[NB][4];
+                    // 0 * sum would not do: a NaN weight stays with its tokens
+                    bool on[NB][2];
+                    float f[NB][2][2];
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            x[nb][b] = make_uint4(0, 0, 0, 0);
-                            if (on[nb])
-                                x[nb][b] = lds128(bp[nb] + b * 64);
+                        for (int j = 0; j < 2; ++j) {
+                            const int row = map[nb * 8 + 2 * c + j];
+                            on[nb][j] = row >= 0;
+                            const float *fi = s_inv + max(row, 0) * chunks + 2 * u;
+                            f[nb][j][0] = fi[0];
+                            f[nb][j][1] = fi[1];
                         }
-                    __syncwarp();  // the stage the loader fills next has been read
-                    ld.issue();
-                    cp_wait<DEPTH - 1>();
+                    __syncwarp();  // the other stage has been read
+                    if (ld.on(plan)) {
+                        down_fill(a, plan, ld.strip, s_sel[ld.is], ld.w * plan.win + ld.u * kSlice,
+                                  ring_s + (st ^ kStageBytes));
+                        ld.next(plan);
+                    } else {
+                        cp_commit();
+                    }
+                    cp_wait<1>();
                     __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float sum[NB][4];
-                        chunk_mma<NB>(sum, st + h * kChunkBytes, a_off,
-                                      [&](int nb, int b) { return x[nb][b]; }, g);
+                    for (int v = 0; v < 2; ++v)
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
+                        for (int h = 0; h < 2; ++h) {
+                            float sum[NB][4];
+                            chunk_mma<NB>(sum, ring_s + st + (2 * h + v) * kChunkBytes, a_off,
+                                          [&](int nb, int b) { return x[nb][4 * v + b]; }, g);
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int row = map[nb * 8 + 2 * c + j];
-                                if (row >= 0) {  // not 0 * sum: a NaN weight stays with its tokens
-                                    const float f = s_inv[row * chunks + at.c];
-                                    acc[h][nb][j] = fmaf(sum[nb][j], f, acc[h][nb][j]);
-                                    acc[h][nb][2 + j] = fmaf(sum[nb][2 + j], f, acc[h][nb][2 + j]);
-                                }
-                            }
-                    }
-                    st = st + kStageBytes == ring_s + DEPTH * kStageBytes ? ring_s : st + kStageBytes;
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (on[nb][j]) {
+                                        acc[h][nb][j] = fmaf(sum[nb][j], f[nb][j][v], acc[h][nb][j]);
+                                        acc[h][nb][2 + j] =
+                                            fmaf(sum[nb][2 + j], f[nb][j][v], acc[h][nb][2 + j]);
+                                    }
+                        }
+                    st ^= kStageBytes;
+                    u += kWarps;
                 }
             }
-            // the warps' sums, 8 NB floats a lane, over GEMM 2's finished rows of h
-            if (plan.n_win == 1 && strip + 1 < plan.strips)
-                staged = false;
+            // the warps' sums over GEMM 2's finished rows of h: [warp][half][nb][lane] float4
             __syncthreads();
-            constexpr int SQ = 8 * NB;
-            float *sums = reinterpret_cast<float *>(region);
-            float4 *o = reinterpret_cast<float4 *>(sums + ((size_t)warp * 32 + lane) * SQ);
+            float4 *o = reinterpret_cast<float4 *>(region) + (size_t)warp * 2 * NB * 32 + lane;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    o[h * NB + nb] = make_float4(acc[h][nb][0], acc[h][nb][1], acc[h][nb][2], acc[h][nb][3]);
+                    o[(h * NB + nb) * 32] =
+                        make_float4(acc[h][nb][0], acc[h][nb][1], acc[h][nb][2], acc[h][nb][3]);
             __syncthreads();
-            for (int j = threadIdx.x; j < kStrip * T; j += kThreads) {
-                const int s = j & (kStrip - 1), t = j / kStrip;
+            const float *sums = reinterpret_cast<const float *>(region);
+#pragma unroll 1
+            for (int j = threadIdx.x; j < 256 * NB; j += kThreads) {
+                // j: [half][nb][row bit 3][lane of the fragment][token bit 0]
+                const int L = j >> 1 & 31, hn = j >> 7, s = (hn / NB) * 16 + (j >> 6 & 1) * 8 + (L >> 2);
+                const int t = hn % NB * 8 + 2 * (L & 3) + (j & 1);
                 const int q = plan.lo + 8 * strip, col = down_column(q, s);
-                if (s < 4 * (plan.hi - q) && col < d) {
-                    const float *r = sums + (size_t)((s & 7) * 4 + (t & 7) / 2) * SQ +
-                                     (s >> 4) * 4 * NB + t / 8 * 4 + (s & 8) / 4 + (t & 1);
+                if (t < T && s < 4 * (plan.hi - q) && col < d) {
+                    const float *r = sums + ((size_t)hn * 32 + L) * 4 + (j >> 6 & 1) * 2 + (j & 1);
                     float v = 0.f;
 #pragma unroll
                     for (int u = 0; u < kWarps; ++u)
-                        v += r[(size_t)u * 32 * SQ];
+                        v += r[(size_t)u * 2 * NB * 128];
                     a.y[(int64_t)t * d + col] = __float2bfloat16_rn(v * a.scale);
                 }
             }
-            if (strip + 1 < plan.strips)
-                __syncthreads();  // the sums are read before h is staged over them
         }
     }
     cp_wait<0>();
 }
 
 // --------------------------------------------------------------------- host side
-
-constexpr int kDepths = 3;
-constexpr int kDepth[kDepths] = {4, 3, 2};  // stages of a warp's ring
-typedef void (*Kernel)(const Args);
-static const Kernel kKernel[2][kDepths] = {
-    {mx4_few_kernel<1, 4>, mx4_few_kernel<1, 3>, mx4_few_kernel<1, 2>},
-    {mx4_few_kernel<2, 4>, mx4_few_kernel<2, 3>, mx4_few_kernel<2, 2>}};
 
 static cudaError_t grid_size(int *out)
 {
@@ -1047,13 +1043,12 @@ static cudaError_t grid_size(int *out)
     std::lock_guard<std::mutex> lk(mu);
     if (sms[dev] == 0) {
         int n = 0;
-        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(mx4_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSmem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(mx4_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSmem)) != cudaSuccess)
             return e;
-        for (int i = 0; i < 2 * kDepths; ++i)
-            if ((e = cudaFuncSetAttribute(kKernel[i / kDepths][i % kDepths],
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)kSmemCap)) != cudaSuccess)
-                return e;
         sms[dev] = n;
     }
     *out = sms[dev];
@@ -1061,17 +1056,21 @@ static cudaError_t grid_size(int *out)
 }
 
 // Columns staged at once for R rows of h of K columns: all of them if they fit the region
-// and the table of scales, else as many whole chunks as do.
+// and the table of scales, else as many whole slices as do.
 static int window(int rows, int K)
 {
-    const int all = (K + kChunkCols - 1) / kChunkCols * kChunkCols;
-    int w = (kMaxRegion / rows - 64) / 2 / kChunkCols * kChunkCols;
-    const int t = kMaxInv / rows * kChunkCols;
+    const int all = (K + kSlice - 1) / kSlice * kSlice;
+    int w = (kRegion / rows - 64) / 2 / kSlice * kSlice;
+    const int t = kMaxInv / rows * kChunkCols / kSlice * kSlice;
     w = w < t ? w : t;
     return w < all ? w : all;
 }
 
 }  // namespace few
+
+static_assert(few::kRegion / few::kMaxRows >= 2 * few::kSlice + 64 &&
+                  few::kMaxInv / few::kMaxRows * few::kChunkCols >= few::kSlice,
+              "a slice of every row of h fits");
 
 bool mx4_few_fits(const moe_params_t *p, bool noisy)
 {
@@ -1122,26 +1121,28 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.k = p->k;
     a.C = p->capacity;
     a.router_type = p->router_type;
-    const int R = p->T * p->k, nb = p->T <= 8 ? 1 : 2;
+    const int R = p->T * p->k;
+    const int64_t r13 = 2 * round_up(p->m, 16);
+    a.tk1 = (p->d + 127) / 128;
+    a.tk2 = (p->m + 127) / 128;
+    a.w13_codes = r13 * (p->d / 2);
+    a.w13_scales = (r13 + 127) / 128 * a.tk1 * kMx4Tile;
+    a.w2_codes = (int64_t)p->d * (mx4_k32(p->m) / 2);
+    a.w2_scales = (int64_t)(p->d + 127) / 128 * a.tk2 * kMx4Tile;
     a.win2 = window(R, p->m);
-    const int h_bytes = R * row_pitch(a.win2);
-    a.region = round_up(h_bytes > kSums ? h_bytes : kSums, 128);
-    int di = 0;
-    while (di + 1 < kDepths && (size_t)a.region + kDepth[di] * kWarps * kStageBytes > kSmemCap)
-        ++di;
-    const size_t smem = (size_t)a.region + kDepth[di] * kWarps * kStageBytes;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launch();
-    e = cudaLaunchKernelEx(&cfg, kKernel[nb - 1][di], a);
+    e = p->T <= 8 ? cudaLaunchKernelEx(&cfg, mx4_few_kernel<1>, a)
+                  : cudaLaunchKernelEx(&cfg, mx4_few_kernel<2>, a);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
