@@ -210,9 +210,17 @@ def _p(t):
     return t.data_ptr() or None
 
 
+# the current stream's handle without building a torch.cuda.Stream (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _device is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 def _dtype_code(dt):
@@ -765,10 +773,15 @@ def _mx4_rows(t):
     return t.data_ptr() or None, G, rows, K, ld
 
 
-def _mx4_bytes(t, n, name):
-    if t.dtype != torch.uint8 or t.numel() != n:
-        raise ValueError("%s must hold %d uint8 elements" % (name, n))
-    return _p(t)
+def _mx4_pair(codes, scales, G, rows, K):
+    """Pointers of a batch's codes and scales, of the right sizes."""
+    n = G * rows * ((K + 31) // 32 * 16)
+    if codes.dtype != torch.uint8 or codes.numel() != n:
+        raise ValueError("codes must hold %d uint8 elements" % n)
+    n = G * ((rows + 127) // 128) * ((K + 127) // 128) * 512
+    if scales.dtype != torch.uint8 or scales.numel() != n:
+        raise ValueError("scales must hold %d uint8 elements" % n)
+    return _p(codes), _p(scales)
 
 
 def moe_mx4_quantize(src, out=None, stream=None):
@@ -779,10 +792,8 @@ def moe_mx4_quantize(src, out=None, stream=None):
         u8 = dict(dtype=torch.uint8, device=src.device)
         out = (torch.empty(G, rows, (K + 31) // 32 * 16, **u8),
                torch.empty(G, (rows + 127) // 128, (K + 127) // 128, 32, 4, 4, **u8))
-    codes, scales = out
-    _check(lib().moe_mx4_quantize(ptr, _dtype_code(src.dtype), G, rows, K, ld,
-                                  _mx4_bytes(codes, moe_mx4_codes_bytes(G, rows, K), "codes"),
-                                  _mx4_bytes(scales, moe_mx4_scales_bytes(G, rows, K), "scales"),
+    codes, scales = _mx4_pair(out[0], out[1], G, rows, K)
+    _check(lib().moe_mx4_quantize(ptr, _dtype_code(src.dtype), G, rows, K, ld, codes, scales,
                                   _stream(stream)))
     return out
 
@@ -796,18 +807,33 @@ def moe_mx4_dequantize(codes, scales, K, dtype=torch.bfloat16, out=None, stream=
     ptr, Go, ro, Ko, ld = _mx4_rows(out)
     if (Go, ro, Ko) != (G, rows, K):
         raise ValueError("out must be [%d][%d][%d]" % (G, rows, K))
-    _check(lib().moe_mx4_dequantize(_mx4_bytes(codes, moe_mx4_codes_bytes(G, rows, K), "codes"),
-                                    _mx4_bytes(scales, moe_mx4_scales_bytes(G, rows, K), "scales"),
-                                    _dtype_code(out.dtype), G, rows, K, ld, ptr,
+    cp, sp = _mx4_pair(codes, scales, G, rows, K)
+    _check(lib().moe_mx4_dequantize(cp, sp, _dtype_code(out.dtype), G, rows, K, ld, ptr,
                                     _stream(stream)))
     return out
 
 
-class Mx4Experts:
+class _Pointers:
+    """Keeps the device pointers of its tensor attributes up to date as they are set, so that
+    a call need not look at every tensor again."""
+
+    def __init__(self, struct):
+        object.__setattr__(self, "_c", struct)
+
+    def __setattr__(self, name, t):
+        if name in self._names:
+            setattr(self._c, name, _p(t) if t is None or t.is_cuda else None)
+        object.__setattr__(self, name, t)
+
+
+class Mx4Experts(_Pointers):
     """The packed expert weights of a layer in mx4: W13_q / W13_s of W13_e [E][2*m16][d] and
     W2_q / W2_s of W2_e [E][d][m8]."""
 
+    _names = ("W13_q", "W13_s", "W2_q", "W2_s")
+
     def __init__(self, W13_q, W13_s, W2_q, W2_s):
+        super().__init__(_Mx4Buffers())
         self.W13_q, self.W13_s, self.W2_q, self.W2_s = W13_q, W13_s, W2_q, W2_s
 
     @classmethod
@@ -825,28 +851,32 @@ def moe_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s, stream=None):
 
 
 def moe_expert_up_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, ws, stream=None):
-    _check(lib().moe_expert_up_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets), _p(W.W13_q),
-                                   _p(W.W13_s), _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
+    _check(lib().moe_expert_up_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
+                                   W._c.W13_q, W._c.W13_s, _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
                                    _stream(stream)))
 
 
 def moe_expert_down_mx4(p, h_q, h_s, offsets, W: Mx4Experts, out, ws, stream=None):
-    _check(lib().moe_expert_down_mx4(C.byref(p), _p(h_q), _p(h_s), _p(offsets), _p(W.W2_q),
-                                     _p(W.W2_s), _p(out), ws.ptr, ws.nbytes, _stream(stream)))
+    _check(lib().moe_expert_down_mx4(C.byref(p), _p(h_q), _p(h_s), _p(offsets),
+                                     W._c.W2_q, W._c.W2_s, _p(out), ws.ptr, ws.nbytes,
+                                     _stream(stream)))
 
 
 def moe_expert_ffn_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, out, ws, stream=None):
-    _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets), _p(W.W13_q),
-                                    _p(W.W13_s), _p(W.W2_q), _p(W.W2_s), _p(h_q), _p(h_s),
+    _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
+                                    W._c.W13_q, W._c.W13_s, W._c.W2_q, W._c.W2_s, _p(h_q), _p(h_s),
                                     _p(out), ws.ptr, ws.nbytes, _stream(stream)))
 
 
-class Mx4Buffers:
+class Mx4Buffers(_Pointers):
     """Outputs and intermediates of moe_forward_mx4 for layer p, allocated with torch.
     ``act`` limits the intermediates to those of one form (None: both).  A tensor given by
     name (Mx4Buffers(p, y=mine)) is used instead of a new one."""
 
+    _names = tuple(_MX4_FIELDS[10:])
+
     def __init__(self, p: Params, act=None, device="cuda", **given):
+        super().__init__(_Mx4Buffers())
         T, d, E, k, m = p.T, p.d, p.E, p.k, p.m
         rows = T * k
         i32, f32, b16, u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
@@ -862,10 +892,10 @@ class Mx4Buffers:
                 shapes[n + "_q"] = ((moe_mx4_rows_bytes(p, K),), u8)
                 shapes[n + "_s"] = ((moe_mx4_row_scales_bytes(p, K),), u8)
             shapes["out"] = ((rows, d), b16)
-        bad = set(given) - set(_MX4_FIELDS[10:])
+        bad = set(given) - set(self._names)
         if bad:
             raise TypeError("not a buffer of moe_forward_mx4: %s" % ", ".join(sorted(bad)))
-        for n in _MX4_FIELDS[10:]:
+        for n in self._names:
             t = given.get(n)
             if t is None and n in shapes:
                 t = torch.empty(shapes[n][0], dtype=shapes[n][1], device=device)
@@ -882,11 +912,10 @@ def moe_forward_mx4(p, x, Wg, W: Mx4Experts, ws, bufs: Mx4Buffers, act=MX4_ACT_B
                     noise=None, bias=None, router_packed=None, stream=None):
     """The whole layer on mx4 expert weights (include/moe.h): at most 16 tokens with bf16
     activations (MX4_ACT_BF16), or any number with quantised rows (MX4_ACT_MX4)."""
-    b = _Mx4Buffers()
-    vals = dict(x=x, Wg=Wg, Wnoise=Wnoise, noise=noise, bias=bias, W13_q=W.W13_q, W13_s=W.W13_s,
-                W2_q=W.W2_q, W2_s=W.W2_s, router_packed=router_packed)
-    for n in _MX4_FIELDS:
-        setattr(b, n, _p(vals[n] if n in vals else getattr(bufs, n)))
+    b, w = bufs._c, W._c
+    b.x, b.Wg, b.Wnoise, b.noise, b.bias = _p(x), _p(Wg), _p(Wnoise), _p(noise), _p(bias)
+    b.W13_q, b.W13_s, b.W2_q, b.W2_s = w.W13_q, w.W13_s, w.W2_q, w.W2_s
+    b.router_packed = _p(router_packed)
     _check(lib().moe_forward_mx4(C.byref(p), C.byref(b), int(act), ws.ptr, ws.nbytes,
                                  _stream(stream)))
     return bufs
