@@ -258,6 +258,9 @@ EXPERT_CASES = [  # T, E, k, m, d, capacity
     (64, 4, 2, 172, 512, -1), (129, 1, 1, 96, 256, -1), (200, 8, 2, 344, 288, -1),
     (300, 5, 2, 130, 224, 50), (700, 3, 2, 200, 1024, -1), (40, 64, 8, 48, 128, -1),
     (256, 2, 1, 1376, 320, -1),
+    # 4096 rows and more: CTA pairs, one or several column tiles, ragged ends
+    (4096, 1, 1, 64, 96, -1), (2100, 3, 2, 200, 320, -1), (1500, 8, 3, 136, 544, 450),
+    (2300, 5, 2, 400, 288, -1), (1100, 16, 4, 260, 64, 290),
 ]
 
 

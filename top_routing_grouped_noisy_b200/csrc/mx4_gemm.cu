@@ -36,7 +36,6 @@ constexpr int BM = 128;
 constexpr int BKB = 128;            // bytes of a stage row: 256 columns
 constexpr int BKC = 256;            // columns of a stage
 constexpr int ACC = 2;
-constexpr int kSfSets = 4;          // scale column sets in TMEM
 constexpr int kSfCols = 24;         // per set: 2 x (4 A + 8 B)
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_THREADS = 320;
@@ -57,7 +56,7 @@ struct Aux {
     int32_t tstart[MOE_MAX_EXPERTS + 1];
 };
 
-template <int BN>
+template <int EPI, int BN>
 struct Geo {
     static constexpr int BT = (BN + 127) / 128;             // B scale tiles of a tile
     static constexpr int A_BYTES = BM * BKB;
@@ -65,16 +64,20 @@ struct Geo {
     static constexpr int SFA = 2 * kMx4Tile;                // two K tiles per stage
     static constexpr int SFB = BT * 2 * kMx4Tile;
     static constexpr int STAGE = A_BYTES + B_BYTES + SFA + SFB;
-    static constexpr int FIXED = 1024 + (int)sizeof(Aux);
+    static constexpr int EPI_BYTES = EPI == EPI_DOWN ? kEpiStageBytes : 0;
+    static constexpr int FIXED = 1024 + EPI_BYTES + (int)sizeof(Aux);
     static constexpr int FIT = (227 * 1024 - FIXED) / STAGE;
     static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
     static constexpr int SMEM = FIXED + STAGES * STAGE;
     static constexpr int SF_COL = ACC * BN;
+    // a set of scale columns per stage: a full stage's last products, and with them the last
+    // use of its set, have completed
+    static constexpr int SETS = STAGES;
     // kind::mxf4, A and B e2m1 K-major, e8m0 scales, M = 128
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                       (1u << 23) | ((uint32_t)(BM >> 7) << 27);
     static_assert(BN % 64 == 0 && STAGE % 1024 == 0, "tile");
-    static_assert(SF_COL + kSfSets * kSfCols <= TMEM_COLS, "TMEM columns");
+    static_assert(SF_COL + SETS * kSfCols <= TMEM_COLS, "TMEM columns");
     static_assert(SMEM > 114 * 1024, "one CTA per SM: TMEM is allocated before the grid wait");
 };
 
@@ -149,16 +152,85 @@ __device__ __forceinline__ void swiglu16(const uint32_t (&v)[32], float *h)
     }
 }
 
+// One block of h (32 neurons from nb on) of this thread's row from its 64 accumulator columns:
+// codes and scale byte.  Neurons past m, whose W rows are not read, are zeros.
+__device__ __forceinline__ uint4 swiglu_block(const uint32_t (&v)[2][32], int nb, int m, uint32_t &byte)
+{
+    float h[32];
+    swiglu16(v[0], h);
+    swiglu16(v[1], h + 16);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (nb + i >= m)
+            h[i] = 0.f;
+        amax = max(amax, __float_as_uint(h[i]) & 0x7fffffffu);
+    }
+    byte = mx4_scale_byte(amax);
+    const float inv = mx4_inverse(byte == 255u ? 0u : byte);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = h[8 * j + i] * inv;
+        c[j] = byte == 255u ? 0u : mx4_codes8(q);
+    }
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// The scale byte of a block of h; with the last block, the rest of its word.
+__device__ __forceinline__ void store_scale(const GemmArgs &a, const Tile &t, int row, int nb,
+                                            uint32_t byte)
+{
+    const int tkh = (2 * a.ld + 127) / 128;
+    uint8_t *sp = a.h_s + mx4_scale_at(mx4_expert_tile(t.off, t.e), tkh, row - t.off, nb / 32);
+    sp[0] = (uint8_t)byte;
+    if (nb + 32 >= 2 * a.ld)
+        for (int b = nb / 32 + 1; b % 4 != 0; ++b)
+            *++sp = 0;
+}
+
+// 64 output columns from col on of this thread's row: boxes wholly inside the expert's rows
+// and the columns through the staging slots, the others per lane.
+__device__ __forceinline__ void store_64(const GemmArgs &a, const uint32_t (&v)[2][32], int col0,
+                                         int row0, int row, int row_end, EpiStore &st)
+{
+#pragma unroll
+    for (int q2 = 0; q2 < 2; ++q2) {
+        const int col = col0 + q2 * 32;
+        if (row0 + 32 <= row_end && col + 32 <= a.n_valid) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = pack_bf16x2(__uint_as_float(v[q2][2 * i]), __uint_as_float(v[q2][2 * i + 1]));
+            stage_box(st, pk, col, row0);
+        } else if (row < row_end) {
+            bf16 *dst = static_cast<bf16 *>(a.out) + (int64_t)row * a.ld + col;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (col + q * 8 < a.n_valid) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = __uint_as_float(v[q2][q * 8 + i]);
+                    st_v4(dst + q * 8, f32x8_to_bf16(f));
+                }
+        }
+    }
+}
+
 template <int EPI, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ GemmArgs a)
+                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ GemmArgs a)
 {
-    using G = Geo<BN>;
+    using G = Geo<EPI, BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    Aux *aux = reinterpret_cast<Aux *>(smem + G::STAGES * G::STAGE);
+    Aux *aux = reinterpret_cast<Aux *>(smem + G::STAGES * G::STAGE + G::EPI_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &aux->abort_flag;
 
@@ -259,7 +331,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // ---------------------------------------------------------- issuer
             int stage = 0;
             uint32_t phase = 0;
-            int acc = 0, set = 0;
+            int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
             const int nk = (a.K32 + 63) / 64;  // products along K
@@ -283,7 +355,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     tc_fence_after();
                     const uint32_t sa = smem_base + stage * G::STAGE, sb = sa + G::A_BYTES;
                     const uint32_t sfa = sb + G::B_BYTES, sfb = sfa + G::SFA;
-                    const uint32_t sf = tmem_base + (uint32_t)(G::SF_COL + set * kSfCols);
+                    const uint32_t sf = tmem_base + (uint32_t)(G::SF_COL + stage * kSfCols);
                     const int halves = min(2, tk - 2 * kb);
                     for (int hh = 0; hh < halves; ++hh) {
                         sf_copy(sf + hh * 12, sfa + hh * kMx4Tile);
@@ -301,8 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                  (kb | k) != 0);
                     }
                     umma_commit(smem_u32(&aux->empty[stage]));
-                    set = (set + 1) % kSfSets;
-                    if (++stage == G::STAGES) {
+                        if (++stage == G::STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -325,6 +396,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // 64-column groups of the tile: the first half of the warps takes the larger half
         constexpr int kGroups = BN / 64, kHalf0 = (kGroups + 1) / 2;
         const int g_first = upper ? kHalf0 : 0, g_end = upper ? kGroups : kHalf0;
+        EpiStore st{&tmO, smem_base + (uint32_t)(G::STAGES * G::STAGE + (warp - 2) * 2 * kStageSlotBytes), 0};
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -344,53 +416,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     tmem_wait_ld();
                     if constexpr (EPI == EPI_UP) {
                         const int nb = t.n0 / 2 + gi * 32;  // 32 neurons: one block of h
-                        float h[32];
-                        swiglu16(v[0], h);
-                        swiglu16(v[1], h + 16);
-                        uint32_t amax = 0;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (nb + i >= a.n_valid)  // neurons past m (their W rows are not read)
-                                h[i] = 0.f;
-                            amax = max(amax, __float_as_uint(h[i]) & 0x7fffffffu);
-                        }
-                        const uint32_t byte = mx4_scale_byte(amax);
-                        const float inv = mx4_inverse(byte == 255u ? 0u : byte);
-                        uint32_t c[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float q[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                q[i] = h[8 * j + i] * inv;
-                            c[j] = byte == 255u ? 0u : mx4_codes8(q);
-                        }
+                        uint32_t byte;
+                        const uint4 c = swiglu_block(v, nb, a.n_valid, byte);
                         if (rv && nb < 2 * a.ld) {
-                            st_v4(static_cast<uint8_t *>(a.out) + (int64_t)row * a.ld + nb / 2,
-                                  make_uint4(c[0], c[1], c[2], c[3]));
-                            const int tkh = (2 * a.ld + 127) / 128;
-                            uint8_t *sp = a.h_s + mx4_scale_at(mx4_expert_tile(t.off, t.e), tkh,
-                                                               row - t.off, nb / 32);
-                            sp[0] = (uint8_t)byte;
-                            if (nb + 32 >= 2 * a.ld)  // the word's bytes past the last block
-                                for (int b = nb / 32 + 1; b % 4 != 0; ++b)
-                                    *++sp = 0;
+                            st_v4(static_cast<uint8_t *>(a.out) + (int64_t)row * a.ld + nb / 2, c);
+                            store_scale(a, t, row, nb, byte);
                         }
-                    } else if (rv) {
-                        bf16 *dst = static_cast<bf16 *>(a.out) + (int64_t)row * a.ld;
-#pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int col = t.n0 + gi * 64 + q2 * 32 + q * 8;
-                                if (col < a.n_valid) {
-                                    float f[8];
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        f[i] = __uint_as_float(v[q2][q * 8 + i]);
-                                    st_v4(dst + col, f32x8_to_bf16(f));
-                                }
-                            }
+                    } else {
+                        store_64(a, v, t.n0 + gi * 64, t.row0 + lane_base, row, t.row_end, st);
                     }
                     __syncwarp();  // the next tcgen05.ld takes the whole warp
                 }
@@ -404,6 +437,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 acc_phase ^= 1u;
             }
         }
+        if (lane == 0)
+            bulk_wait_all();  // this lane's output stores are done before the CTA exits
     }
     tc_fence_before();
     __syncthreads();
@@ -415,14 +450,451 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 }
 
+// ------------------------------------------------------------------------ 2-SM variant
+// cta_group::2: a cluster of two CTAs owns a 256 x 256 tile.  CTA r loads rows [128r, 128r +
+// 128) of A and of B with A's scales for its rows and B's for all 256 (every CTA's
+// accumulators see all columns); the leader issues M = 256 products.  The 1-SM kernel is bound
+// by the bytes that L2 hands to the SMs (43 KB per 128 x 192 x 256, about 30 bytes a cycle and
+// SM); here 35 KB serve 128 x 256 x 256 of each SM's work.
+//
+// TMEM.  Two 256-column accumulators do not leave room for scales, so they share 64 columns:
+// accumulator 0 is columns 0..255, accumulator 1 columns 192..447, scales 448..495 (two sets).
+// The epilogue reads the shared 64 columns first and then lets the next tile's products
+// start; the tile before (the same accumulator) is read by then, since every warp takes the
+// tiles in order.  A set of scales is copied over only after the products of two stages ago
+// have completed (sfree), so nothing rests on the order of copies after products.
+//   full[s]   leader: both CTAs' bytes          empty[s]  both CTAs: the leader's commit
+//   tfull[a]  both CTAs: the leader's commit    tfree     leader: 8 epilogue warps of each CTA
+//   sfree[i]  leader: its own commit
+// Loads carry no multicast qualifier.
+namespace pair {
+
+constexpr int BN = 256;
+constexpr int BNH = 128;
+constexpr int A_BYTES = BM * BKB;
+constexpr int B_BYTES = BNH * BKB;
+constexpr int SFA = 2 * kMx4Tile;
+constexpr int SFB = 2 * 2 * kMx4Tile;
+constexpr int STAGE = A_BYTES + B_BYTES + SFA + SFB;
+constexpr int ACC_STEP = 192;              // accumulator 1 starts here
+constexpr int SF_COL = ACC_STEP + BN;      // 448
+constexpr uint64_t kAbortSettleNs = 200000ull;
+constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
+                            ((uint32_t)(256 >> 7) << 27);
+static_assert(SF_COL + 2 * kSfCols <= TMEM_COLS, "TMEM columns");
+static_assert(STAGE % 1024 == 0, "stage alignment");
+
+template <int EPI>
+struct Geo {
+    static constexpr int EPI_BYTES = EPI == EPI_DOWN ? kEpiStageBytes : 0;
+    static constexpr int STAGES = EPI == EPI_DOWN ? 5 : 6;
+};
+
+struct Aux {
+    uint64_t full[6];
+    uint64_t empty[6];
+    uint64_t tfull[2];
+    uint64_t tfree;
+    uint64_t sfree[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t off[MOE_MAX_EXPERTS + 1];
+    int32_t tstart[MOE_MAX_EXPERTS + 1];
+};
+template <int EPI>
+constexpr int smem_bytes() { return 1024 + Geo<EPI>::STAGES * STAGE + Geo<EPI>::EPI_BYTES + (int)sizeof(Aux); }
+static_assert(smem_bytes<EPI_UP>() <= 227 * 1024 && smem_bytes<EPI_DOWN>() <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t cluster_addr)
+{
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void load_2d(const CUtensorMap *map, uint32_t bar_cluster, uint32_t dst,
+                                        int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(const CUtensorMap *map, uint32_t bar_cluster, uint32_t dst,
+                                        int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// scale tile to the TMEM of both CTAs, each from its own shared memory
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t saddr)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(saddr))
+                 : "memory");
+}
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t sfa, uint32_t sfb, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_both(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void commit_own(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bar)
+                 : "memory");
+}
+
+// Tile order inside an expert: bands of `band` row tiles, row tiles fastest inside a band,
+// then the band's column tiles (as in the bf16 pair kernel).
+__device__ __forceinline__ Tile decode(const Aux *aux, int tile, int n_tiles, int band)
+{
+    Tile t;
+    int e = 0;
+    while (tile >= aux->tstart[e + 1])
+        ++e;
+    const int local = tile - aux->tstart[e];
+    const int rows = aux->off[e + 1] - aux->off[e];
+    const int mtiles = (rows + 2 * BM - 1) / (2 * BM);
+    int G = (band > 0 && band < mtiles) ? band : mtiles;
+    const int nbands = (mtiles + G - 1) / G;
+    G = (mtiles + nbands - 1) / nbands;
+    const int bi = local / (G * n_tiles);
+    const int rem = local - bi * G * n_tiles;
+    const int gr = mtiles - bi * G < G ? mtiles - bi * G : G;
+    t.e = e;
+    t.off = aux->off[e];
+    t.row0 = t.off + (bi * G + rem % gr) * 2 * BM;
+    t.row_end = aux->off[e + 1];
+    t.n0 = rem / gr * BN;
+    return t;
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    mx4_gemm_2sm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSA,
+                        const __grid_constant__ CUtensorMap tmSB,
+                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ GemmArgs a,
+                        int band)
+{
+    constexpr int STAGES = Geo<EPI>::STAGES;
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    Aux *aux = reinterpret_cast<Aux *>(smem + STAGES * STAGE + Geo<EPI>::EPI_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int32_t *abort_flag = &aux->abort_flag;
+    const uint32_t rank = cta_rank();
+    const bool leader = rank == 0;
+    const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&aux->full[s]), 1);
+            mbar_init(smem_u32(&aux->empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&aux->tfull[i]), 1);
+            mbar_init(smem_u32(&aux->sfree[i]), 1);
+        }
+        mbar_init(smem_u32(&aux->tfree), 2 * EPI_WARPS);
+        mbar_init(smem_u32(&aux->drain), 1);
+        aux->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        const CUtensorMap *maps[5] = {&tmA, &tmB, &tmSA, &tmSB, &tmO};
+        for (int i = 0; i < (EPI == EPI_DOWN ? 5 : 4); ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
+    }
+    const int n_tiles = (a.N + BN - 1) / BN;
+    if (warp == 2) {
+        for (int i = lane; i <= a.E; i += 32)
+            aux->off[i] = a.offsets[i];
+        __syncwarp();
+        if (lane == 0) {
+            int acc = 0;
+            for (int e = 0; e < a.E; ++e) {
+                aux->tstart[e] = acc;
+                acc += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM) * n_tiles;
+            }
+            aux->tstart[a.E] = acc;
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&aux->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = aux->tmem_base;
+    const int total = aux->tstart[a.E];
+    const int num_kb = (a.K32 + BKC - 1) / BKC;
+    const int trb = (a.N + 127) / 128;
+    const uint32_t smem_base = smem_u32(smem);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------------------------------------------------- TMA producer (both)
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t fills = 0;
+            bool ok = true;
+            for (int tile = cluster_id; tile < total && ok; tile += nclusters) {
+                const Tile t = decode(aux, tile, n_tiles, band);
+                const int sa_row = (int)mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM + (int)rank;
+                const int sb_row = t.e * trb + t.n0 / 128;
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                                   a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&aux->full[stage]), fb0 = map_rank(fb, 0);
+                    if (leader)
+                        mbar_expect_tx(fb, 2 * STAGE);
+                    const uint32_t sa = smem_base + stage * STAGE, sb = sa + A_BYTES;
+                    load_2d(&tmA, fb0, sa, kb * (BKB / 2), t.row0 + (int)rank * BM);
+                    load_3d(&tmB, fb0, sb, kb * (BKB / 2), t.n0 + (int)rank * BNH, t.e);
+                    load_2d(&tmSA, fb0, sb + B_BYTES, kb * 256, sa_row);
+                    load_2d(&tmSB, fb0, sb + B_BYTES + SFA, kb * 256, sb_row);
+                    ++fills;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (leader)  // the leader's full barriers count both CTAs' bytes
+                for (int s = 0; s < STAGES; ++s) {
+                    const int64_t n = fills / STAGES + (s < fills % STAGES ? 1 : 0);
+                    if (n > 0)
+                        mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------------------------------------------------- issuer (leader)
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t n_st = 0;  // stages issued
+            int ti = 0;        // tiles issued
+            bool ok = true;
+            const int nk = (a.K32 + 63) / 64;
+            for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++ti) {
+                // the shared columns of the tile before have been read
+                if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                                         abort_flag, a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)((ti & 1) * ACC_STEP);
+                for (int kb = 0; kb < num_kb; ++kb, ++n_st) {
+                    const int set = (int)(n_st & 1);
+                    if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                                   a.status) ||
+                        (n_st >= 2 && !mbar_wait(smem_u32(&aux->sfree[set]),
+                                                 (uint32_t)(n_st / 2 - 1) & 1u, a.wait_ns,
+                                                 abort_flag, a.status))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_base + stage * STAGE, sb = sa + A_BYTES;
+                    const uint32_t sfa = sb + B_BYTES, sfb = sfa + SFA;
+                    const uint32_t sf = tmem_base + (uint32_t)(SF_COL + set * kSfCols);
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        sf_copy(sf + hh * 12, sfa + hh * kMx4Tile);
+                        sf_copy(sf + hh * 12 + 4, sfb + hh * kMx4Tile);
+                        sf_copy(sf + hh * 12 + 8, sfb + (2 + hh) * kMx4Tile);
+                    }
+                    const uint64_t da = sdesc(sa), db = sdesc(sb);
+                    const int ks = min(4, nk - 4 * kb);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= ks)
+                            break;
+                        const uint32_t id = (uint32_t)(k & 1) * 2u;
+                        const uint32_t col = sf + (uint32_t)(k >> 1) * 12;
+                        umma(d_tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
+                             kIdesc | (id << 4) | (id << 29), col, col + 4, (kb | k) != 0);
+                    }
+                    commit_both(smem_u32(&aux->empty[stage]));
+                    commit_own(smem_u32(&aux->sfree[set]));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                commit_both(smem_u32(&aux->tfull[ti & 1]));
+            }
+            commit_own(smem_u32(&aux->drain));
+            mbar_drain(smem_u32(&aux->drain), 0);
+        }
+    } else {
+        // -------------------------------------------------------------- epilogue (both)
+        const int lane_base = (warp & 3) * 32;
+        const int half = (warp - 2) / 4;  // 64-column groups 2 half, 2 half + 1
+        const uint32_t tfree0 = map_rank(smem_u32(&aux->tfree), 0);
+        EpiStore st{&tmO, smem_base + (uint32_t)(STAGES * STAGE + (warp - 2) * 2 * kStageSlotBytes), 0};
+        int ti = 0;
+        for (int tile = cluster_id; tile < total; tile += nclusters, ++ti) {
+            const Tile t = decode(aux, tile, n_tiles, band);
+            const int acc = ti & 1;
+            if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+                           a.status))
+                break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * ACC_STEP);
+            const int row0 = t.row0 + (int)rank * BM + lane_base, row = row0 + lane;
+            const bool rv = row < t.row_end;
+            // the shared columns are group 3 of accumulator 0 and group 0 of accumulator 1: the
+            // half that has them takes them first
+            const bool shares = half == 1 - acc;
+            if (!shares && lane == 0)
+                mbar_arrive_cluster(tfree0);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
+                uint32_t v[2][32];
+                tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
+                tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
+                tmem_wait_ld();
+                if (shares && i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(tfree0);
+                }
+                if constexpr (EPI == EPI_UP) {
+                    const int nb = t.n0 / 2 + gi * 32;  // 32 neurons: one block of h
+                    uint32_t byte;
+                    const uint4 c = swiglu_block(v, nb, a.n_valid, byte);
+                    if (rv && nb < 2 * a.ld) {
+                        st_v4(static_cast<uint8_t *>(a.out) + (int64_t)row * a.ld + nb / 2, c);
+                        store_scale(a, t, row, nb, byte);
+                    }
+                } else {
+                    store_64(a, v, t.n0 + gi * 64, row0, row, t.row_end, st);
+                }
+                __syncwarp();  // the next tcgen05.ld takes the whole warp
+            }
+        }
+        if (lane == 0)
+            bulk_wait_all();  // this lane's output stores are done before the CTA exits
+    }
+    tc_fence_before();
+    cluster_sync();
+    // after an abort, give copies still in flight time to land before either CTA of
+    // the pair releases its shared memory (the other CTA's loads signal the leader)
+    if (threadIdx.x == 0) {
+        const int peer_abort = ld_cluster_s32(map_rank(smem_u32(&aux->abort_flag), rank ^ 1u));
+        if (*abort_flag || peer_abort) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kAbortSettleNs) {
+            }
+        }
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+}  // namespace pair
+
 // ------------------------------------------------------------------------ host side
 
 struct DevInfo {
     int sms = 0;
+    int pair_clusters = 0;
 };
 static std::mutex g_mu;
 static DevInfo g_dev[64];
 
+template <typename Kern>
+static cudaError_t allow_smem(Kern kern, int bytes)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int BN>
+static cudaError_t allow_smem_1sm()
+{
+    const cudaError_t e = allow_smem(mx4_gemm_kernel<EPI_UP, BN>, Geo<EPI_UP, BN>::SMEM);
+    return e != cudaSuccess ? e : allow_smem(mx4_gemm_kernel<EPI_DOWN, BN>, Geo<EPI_DOWN, BN>::SMEM);
+}
+
+static void cluster_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int clusters, int smem,
+                           cudaStream_t s)
+{
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->gridDim = dim3(2 * clusters);
+    cfg->blockDim = dim3(NUM_THREADS);
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = s;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
+
+// SM count, shared-memory opt-in of the kernels, clusters of the pair kernel that fit at once
+// (per device, cached)
 static cudaError_t prepare_device(DevInfo **out)
 {
     int dev = 0;
@@ -434,42 +906,115 @@ static cudaError_t prepare_device(DevInfo **out)
     std::lock_guard<std::mutex> lk(g_mu);
     DevInfo &di = g_dev[dev];
     if (di.sms == 0) {
-        int sms = 0;
+        int sms = 0, n = 0;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(mx4_gemm_kernel<EPI_UP, 192>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      Geo<192>::SMEM)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(mx4_gemm_kernel<EPI_DOWN, 192>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      Geo<192>::SMEM)) != cudaSuccess)
+            (e = allow_smem_1sm<64>()) != cudaSuccess || (e = allow_smem_1sm<128>()) != cudaSuccess ||
+            (e = allow_smem_1sm<192>()) != cudaSuccess ||
+            (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_UP>, pair::smem_bytes<EPI_UP>())) !=
+                cudaSuccess ||
+            (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_DOWN>, pair::smem_bytes<EPI_DOWN>())) !=
+                cudaSuccess)
             return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        cluster_config(&cfg, attr, sms / 2, pair::smem_bytes<EPI_UP>(), nullptr);
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, pair::mx4_gemm_2sm_kernel<EPI_UP>, &cfg)) !=
+            cudaSuccess)
+            return e;
+        di.pair_clusters = n > 0 ? n : 1;
         di.sms = sms;
     }
     *out = &di;
     return cudaSuccess;
 }
 
+// rank-2 map of a scale buffer (4-byte elements, boxes of 1024 bytes x `rows` tile rows)
+static cudaError_t scale_map(CUtensorMap *map, const void *base, uint64_t tk, uint64_t tile_rows,
+                             uint32_t rows)
+{
+    cudaError_t err;
+    EncodeTiledFn enc = get_encoder(&err);
+    if (enc == nullptr)
+        return err != cudaSuccess ? err : cudaErrorSymbolNotFound;
+    const cuuint64_t gd[2] = {tk * (kMx4Tile / 4), tile_rows}, gs[1] = {tk * kMx4Tile};
+    const cuuint32_t bx[2] = {256, rows}, es[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), gd, gs, bx,
+                           es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows (T*k) from which the 2-SM kernel is used; below it the 1-SM kernel spreads the few
+// tiles over more SMs.
+constexpr int64_t kPairMinRows = 4096;
+
+template <int EPI, int BN>
+static cudaError_t launch_1sm(const DevInfo &di, const CUtensorMap &ta, const CUtensorMap &tb,
+                              const CUtensorMap &to, const GemmArgs &args, cudaStream_t s)
+{
+    return launch_pdl(mx4_gemm_kernel<EPI, BN>, dim3(di.sms), dim3(NUM_THREADS),
+                      Geo<EPI, BN>::SMEM, s, ta, tb, to, args);
+}
+
 template <int EPI>
-static cudaError_t launch_gemm(const void *A, uint64_t rows, const void *B, const GemmArgs &args,
+static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const GemmArgs &args,
                                cudaStream_t s)
 {
     DevInfo *di = nullptr;
     cudaError_t e = prepare_device(&di);
     if (e != cudaSuccess)
         return e;
-    constexpr int BN = 192;
+    const bool two = rows >= kPairMinRows;
+    // 1-SM tile width: the fewest columns on the busiest SM when every reached expert has one
+    // row tile, the wider of equal ones
+    int bn = 192;
+    if (!two) {
+        const int64_t hit = rows < args.E ? rows : args.E;
+        int64_t best = INT64_MAX;
+        for (int w : {192, 128, 64}) {
+            const int64_t tiles = hit * ((args.N + w - 1) / w);
+            const int64_t cost = (tiles + di->sms - 1) / di->sms * w;
+            if (cost < best) {
+                best = cost;
+                bn = w;
+            }
+        }
+    }
     // code rows as 2-byte elements (four codes each): the maps only copy
     const uint64_t kel = (uint64_t)args.K32 / 4, pitch = (uint64_t)args.K32 / 2;
-    CUtensorMap ta, tb;
-    const uint64_t da[2] = {kel, rows}, sa[1] = {pitch};
+    CUtensorMap ta, tb, to = {};
+    const uint64_t da[2] = {kel, (uint64_t)rows}, sa[1] = {pitch};
     const uint64_t db[3] = {kel, (uint64_t)args.N, (uint64_t)args.E};
     const uint64_t sb[2] = {pitch, pitch * args.N};
-    const uint32_t ba[2] = {BKB / 2, BM}, bb[3] = {BKB / 2, BN, 1};
+    const uint32_t ba[2] = {BKB / 2, BM}, bb[3] = {BKB / 2, (uint32_t)(two ? pair::BNH : bn), 1};
     if ((e = make_map(&ta, A, 2, da, sa, ba)) != cudaSuccess ||
         (e = make_map(&tb, B, 3, db, sb, bb)) != cudaSuccess)
         return e;
-    return launch_pdl(mx4_gemm_kernel<EPI, BN>, dim3(di->sms), dim3(NUM_THREADS), Geo<BN>::SMEM, s,
-                      ta, tb, args);
+    if (EPI == EPI_DOWN) {  // output boxes of 32 columns x 32 rows
+        const uint64_t dout[2] = {(uint64_t)args.n_valid, (uint64_t)rows}, sout[1] = {(uint64_t)args.ld * 2};
+        const uint32_t bout[2] = {32, 32};
+        if ((e = make_map(&to, args.out, 2, dout, sout, bout, CU_TENSOR_MAP_SWIZZLE_64B)) != cudaSuccess)
+            return e;
+    }
+    if (!two) {
+        if (bn == 64)
+            return launch_1sm<EPI, 64>(*di, ta, tb, to, args, s);
+        if (bn == 128)
+            return launch_1sm<EPI, 128>(*di, ta, tb, to, args, s);
+        return launch_1sm<EPI, 192>(*di, ta, tb, to, args, s);
+    }
+    CUtensorMap tsa, tsb;
+    const uint64_t tk = (args.K32 + 127) / 128;
+    if ((e = scale_map(&tsa, args.a_s, tk, (uint64_t)mx4_row_tiles(rows, args.E), 1)) != cudaSuccess ||
+        (e = scale_map(&tsb, args.b_s, tk, (uint64_t)args.E * ((args.N + 127) / 128), 2)) != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cluster_config(&cfg, attr, di->pair_clusters, pair::smem_bytes<EPI>(), s);
+    const int band_rows = gemm_band_rows();
+    const int band = band_rows <= 0 ? 0 : (band_rows + 2 * BM - 1) / (2 * BM);
+    return cudaLaunchKernelEx(&cfg, pair::mx4_gemm_2sm_kernel<EPI>, ta, tb, tsa, tsb, to, args, band);
 }
 
 }  // namespace mxg
@@ -492,7 +1037,7 @@ cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
     a.status = status;
     a.wait_ns = wait_limit_ns();
     count_launch();
-    return mxg::launch_gemm<mxg::EPI_UP>(xq, (uint64_t)p->T * p->k, W13q, a, s);
+    return mxg::launch_gemm<mxg::EPI_UP>(xq, (int64_t)p->T * p->k, W13q, a, s);
 }
 
 cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *hs,
@@ -512,7 +1057,7 @@ cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *h
     a.status = status;
     a.wait_ns = wait_limit_ns();
     count_launch();
-    return mxg::launch_gemm<mxg::EPI_DOWN>(hq, (uint64_t)p->T * p->k, W2q, a, s);
+    return mxg::launch_gemm<mxg::EPI_DOWN>(hq, (int64_t)p->T * p->k, W2q, a, s);
 }
 
 }  // namespace moe

@@ -255,6 +255,42 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32])
 }
 
 
+// Output staging: each epilogue warp owns two 2 KB shared-memory slots, each one
+// [32 rows][64 bytes] box laid out with the 64-byte swizzle (16-byte chunk j of row
+// r at r*64 + ((j ^ ((r >> 1) & 3)) * 16)), the layout the output tensor map's
+// SWIZZLE_64B expects; the 32 lanes write their rows without bank conflicts.
+constexpr int kStageSlotBytes = 32 * 64;
+constexpr int kEpiStageBytes = 8 /* warps */ * 2 * kStageSlotBytes;
+
+struct EpiStore {
+    const CUtensorMap *map;  // output [rows][cols], box {32 cols, 32 rows}, SWIZZLE_64B
+    uint32_t slots;          // this warp's two slots (1024-byte aligned)
+    int slot;                // slot to use next
+};
+
+// Writes 32 bf16 values (16 packed words) of this lane's row into the next slot and
+// stores the warp's 32 x 32 box at (col, row0) with one bulk tensor store.
+__device__ __forceinline__ void stage_box(EpiStore &st, const uint32_t (&pk)[16], int col, int row0)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+        bulk_wait_read_1();  // the slot's previous store has finished reading it
+    __syncwarp();
+    const uint32_t base = st.slots + (uint32_t)(st.slot * kStageSlotBytes) + (uint32_t)(lane * 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        st_shared_v4(base + (uint32_t)(((j ^ ((lane >> 1) & 3)) << 4)), pk[4 * j], pk[4 * j + 1],
+                     pk[4 * j + 2], pk[4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d_evict_first(st.map, st.slots + (uint32_t)(st.slot * kStageSlotBytes), col,
+                                 row0);
+        bulk_commit();
+    }
+    st.slot ^= 1;
+}
+
 // ------------------------------------------------------------------------ host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
