@@ -81,16 +81,36 @@ struct Geo {
     static_assert(SMEM > 114 * 1024, "one CTA per SM: TMEM is allocated before the grid wait");
 };
 
-// smem descriptor of a scale tile: 32 rows of 16 bytes, no swizzle, 8-row groups 128 B apart
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr)
+// The producer and the issuer run their loops as whole warps and let one elected lane issue:
+// the loops' values stay in uniform registers, where copies and products take their operands
+// (a loop of one lane spends about 450 cycles a stage on moving them, as long as the
+// products take).  The warp number is made uniform the same way.
+__device__ __forceinline__ bool elect_one()
 {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int warp_number()
+{
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 }
 
-__device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t saddr)
+// Descriptors, low and high words (bit 16 of the low word: the leading byte offset, unused by
+// the swizzled tiles and absent from the scale tiles').  Operand tiles: K-major, 128-byte swizzle (as tc::sdesc);
+// scale tiles: 32 rows of 16 bytes, no swizzle, 8-row groups 128 bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kSfDescHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(saddr))
-                 : "memory");
+    return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint64_t sd)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sd) : "memory");
 }
 
 __device__ __forceinline__ void umma_mx4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -231,7 +251,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     Aux *aux = reinterpret_cast<Aux *>(smem + G::STAGES * G::STAGE + G::EPI_BYTES);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &aux->abort_flag;
 
     if (threadIdx.x == 0) {
@@ -283,29 +303,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t smem_base = smem_u32(smem);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------------------------------------- TMA producer
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t fills = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                const Tile t = decode_tile<BN>(aux, tile);
-                const uint8_t *sa_src =
-                    a.a_s + (mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM) * tk * kMx4Tile;
-                const int nb0 = t.n0 / 128;
-                const int nbt = min(G::BT, trb - nb0);  // B scale tiles that exist
-                const uint8_t *sb_src = a.b_s + ((int64_t)t.e * trb + nb0) * tk * kMx4Tile;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
-                                   a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&aux->full[stage]);
-                    const uint32_t sa = smem_base + stage * G::STAGE, sb = sa + G::A_BYTES;
-                    const uint32_t sfa = sb + G::B_BYTES, sfb = sfa + G::SFA;
-                    const uint32_t kt = (uint32_t)min(2, tk - 2 * kb) * kMx4Tile;
+        // -------------------------------------------------------------- TMA producer
+        const bool lead = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t fills = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+            const Tile t = decode_tile<BN>(aux, tile);
+            const uint8_t *sa_src =
+                a.a_s + (mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM) * tk * kMx4Tile;
+            const int nb0 = t.n0 / 128;
+            const int nbt = min(G::BT, trb - nb0);  // B scale tiles that exist
+            const uint8_t *sb_src = a.b_s + ((int64_t)t.e * trb + nb0) * tk * kMx4Tile;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                               a.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&aux->full[stage]);
+                const uint32_t sa = smem_base + stage * G::STAGE, sb = sa + G::A_BYTES;
+                const uint32_t sfa = sb + G::B_BYTES, sfb = sfa + G::SFA;
+                const uint32_t kt = (uint32_t)min(2, tk - 2 * kb) * kMx4Tile;
+                if (lead) {
                     mbar_expect_tx(fb, (uint32_t)(G::A_BYTES + G::B_BYTES) + kt * (1 + nbt));
                     tma_load_2d(&tmA, fb, sa, kb * (BKB / 2), t.row0);
                     tma_load_3d(&tmB, fb, sb, kb * (BKB / 2), t.n0, t.e);
@@ -313,82 +334,88 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int i = 0; i < nbt; ++i)
                         bulk_load(sfb + i * 2 * kMx4Tile,
                                   sb_src + ((int64_t)i * tk + 2 * kb) * kMx4Tile, kt, fb);
-                    ++fills;
-                    if (++stage == G::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                ++fills;
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            for (int s = 0; s < G::STAGES; ++s) {
-                const int64_t n = fills / G::STAGES + (s < fills % G::STAGES ? 1 : 0);
-                if (n > 0)
-                    mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
-            }
+        }
+        for (int s = 0; s < G::STAGES; ++s) {
+            const int64_t n = fills / G::STAGES + (s < fills % G::STAGES ? 1 : 0);
+            if (n > 0)
+                mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------------------------------------------------- issuer
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t acc_phase = 0;
-            bool ok = true;
-            const int nk = (a.K32 + 63) / 64;  // products along K
-            for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-                const Tile t = decode_tile<BN>(aux, tile);
-                // first B scale column inside the copied tiles: one column per 32 rows
-                const uint32_t b_shift = (uint32_t)(t.n0 % 128 / 32);
-                if (!mbar_wait(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
-                               a.status)) {
+        // -------------------------------------------------------------- issuer
+        const bool lead = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        const int nk = (a.K32 + 63) / 64;  // products along K
+        const uint32_t lo0 = desc_lo(smem_base);
+        for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+            const Tile t = decode_tile<BN>(aux, tile);
+            // first B scale column inside the copied tiles: one column per 32 rows
+            const uint32_t b_shift = (uint32_t)(t.n0 % 128 / 32);
+            if (!mbar_wait(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
+                           a.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
-                                   a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_base + stage * G::STAGE, sb = sa + G::A_BYTES;
-                    const uint32_t sfa = sb + G::B_BYTES, sfb = sfa + G::SFA;
-                    const uint32_t sf = tmem_base + (uint32_t)(G::SF_COL + stage * kSfCols);
-                    const int halves = min(2, tk - 2 * kb);
-                    for (int hh = 0; hh < halves; ++hh) {
-                        sf_copy(sf + hh * 12, sfa + hh * kMx4Tile);
+                const uint32_t la = lo0 + (uint32_t)(stage * (G::STAGE >> 4));
+                const uint32_t lb = la + (G::A_BYTES >> 4);
+                const uint32_t lsa = lb + (G::B_BYTES >> 4) - (1u << 16), lsb = lsa + (G::SFA >> 4);
+                const uint32_t sf = tmem_base + (uint32_t)(G::SF_COL + stage * kSfCols);
+                const int halves = min(2, tk - 2 * kb), ks = min(4, nk - 4 * kb);
+                if (lead) {
 #pragma unroll
-                        for (int i = 0; i < G::BT; ++i)
-                            sf_copy(sf + hh * 12 + 4 + i * 4, sfb + (i * 2 + hh) * kMx4Tile);
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (hh < halves) {
+                            sf_copy(sf + hh * 12, desc(lsa + hh * (kMx4Tile >> 4), kSfDescHi));
+#pragma unroll
+                            for (int i = 0; i < G::BT; ++i)
+                                sf_copy(sf + hh * 12 + 4 + i * 4,
+                                        desc(lsb + (i * 2 + hh) * (kMx4Tile >> 4), kSfDescHi));
+                        }
                     }
-                    const uint64_t da = sdesc(sa), db = sdesc(sb);
-                    const int ks = min(4, nk - 4 * kb);
-                    for (int k = 0; k < ks; ++k) {
-                        const uint32_t id = (uint32_t)(k & 1) * 2u;
-                        const uint32_t col = sf + (uint32_t)(k >> 1) * 12;
-                        umma_mx4(d_tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
-                                 G::IDESC | (id << 4) | (id << 29), col, col + 4 + b_shift,
-                                 (kb | k) != 0);
-                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < ks) {
+                            const uint32_t id = (uint32_t)(k & 1) * 2u, col = sf + (uint32_t)(k >> 1) * 12;
+                            umma_mx4(d_tmem, desc(la + 2 * k, kDescHi), desc(lb + 2 * k, kDescHi),
+                                     G::IDESC | (id << 4) | (id << 29), col, col + 4 + b_shift,
+                                     (kb | k) != 0);
+                        }
                     umma_commit(smem_u32(&aux->empty[stage]));
-                        if (++stage == G::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-                if (!ok)
-                    break;
-                umma_commit(smem_u32(&aux->tfull[acc]));
-                if (++acc == ACC) {
-                    acc = 0;
-                    acc_phase ^= 1u;
+                if (++stage == G::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            umma_commit(smem_u32(&aux->drain));
-            mbar_drain(smem_u32(&aux->drain), 0);
+            if (!ok)
+                break;
+            if (lead)
+                umma_commit(smem_u32(&aux->tfull[acc]));
+            if (++acc == ACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
         }
+        if (lead)
+            umma_commit(smem_u32(&aux->drain));
+        mbar_drain(smem_u32(&aux->drain), 0);
     } else {
         // -------------------------------------------------------------- epilogue
         const int lane_base = (warp & 3) * 32;
@@ -458,14 +485,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // SM); here 35 KB serve 128 x 256 x 256 of each SM's work.
 //
 // TMEM.  Two 256-column accumulators do not leave room for scales, so they share 64 columns:
-// accumulator 0 is columns 0..255, accumulator 1 columns 192..447, scales 448..495 (two sets).
+// accumulator 0 is columns 0..255, accumulator 1 columns 192..447, scales 448..471 and 480..503
+// (two sets).
 // The epilogue reads the shared 64 columns first and then lets the next tile's products
 // start; the tile before (the same accumulator) is read by then, since every warp takes the
 // tiles in order.  A set of scales is copied over only after the products of two stages ago
-// have completed (sfree), so nothing rests on the order of copies after products.
+// have completed (its empty barrier), so nothing rests on the order of copies after products.
 //   full[s]   leader: both CTAs' bytes          empty[s]  both CTAs: the leader's commit
 //   tfull[a]  both CTAs: the leader's commit    tfree     leader: 8 epilogue warps of each CTA
-//   sfree[i]  leader: its own commit
 // Loads carry no multicast qualifier.
 namespace pair {
 
@@ -481,7 +508,7 @@ constexpr int SF_COL = ACC_STEP + BN;      // 448
 constexpr uint64_t kAbortSettleNs = 200000ull;
 constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) |
                             ((uint32_t)(256 >> 7) << 27);
-static_assert(SF_COL + 2 * kSfCols <= TMEM_COLS, "TMEM columns");
+static_assert(SF_COL + 32 + kSfCols <= TMEM_COLS, "TMEM columns");
 static_assert(STAGE % 1024 == 0, "stage alignment");
 
 template <int EPI>
@@ -495,7 +522,6 @@ struct Aux {
     uint64_t empty[6];
     uint64_t tfull[2];
     uint64_t tfree;
-    uint64_t sfree[2];
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -553,10 +579,9 @@ __device__ __forceinline__ void load_3d(const CUtensorMap *map, uint32_t bar_clu
         : "memory");
 }
 // scale tile to the TMEM of both CTAs, each from its own shared memory
-__device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t saddr)
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint64_t sd)
 {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sf_desc(saddr))
-                 : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sd) : "memory");
 }
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                      uint32_t sfa, uint32_t sfb, uint32_t acc)
@@ -624,7 +649,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     Aux *aux = reinterpret_cast<Aux *>(smem + STAGES * STAGE + Geo<EPI>::EPI_BYTES);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &aux->abort_flag;
     const uint32_t rank = cta_rank();
     const bool leader = rank == 0;
@@ -635,10 +660,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(smem_u32(&aux->full[s]), 1);
             mbar_init(smem_u32(&aux->empty[s]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
             mbar_init(smem_u32(&aux->tfull[i]), 1);
-            mbar_init(smem_u32(&aux->sfree[i]), 1);
-        }
         mbar_init(smem_u32(&aux->tfree), 2 * EPI_WARPS);
         mbar_init(smem_u32(&aux->drain), 1);
         aux->abort_flag = 0;
@@ -678,53 +701,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t smem_base = smem_u32(smem);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------------------------------------- TMA producer (both)
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t fills = 0;
-            bool ok = true;
-            for (int tile = cluster_id; tile < total && ok; tile += nclusters) {
-                const Tile t = decode(aux, tile, n_tiles, band);
-                const int sa_row = (int)mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM + (int)rank;
-                const int sb_row = t.e * trb + t.n0 / 128;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
-                                   a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&aux->full[stage]), fb0 = map_rank(fb, 0);
+        // -------------------------------------------------------------- TMA producer (both)
+        const bool lead = elect_one();
+        const uint32_t full0 = map_rank(smem_u32(&aux->full[0]), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        int64_t fills = 0;
+        bool ok = true;
+        for (int tile = cluster_id; tile < total && ok; tile += nclusters) {
+            const Tile t = decode(aux, tile, n_tiles, band);
+            const int a_row = t.row0 + (int)rank * BM, b_row = t.n0 + (int)rank * BNH;
+            const int sa_row = (int)mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM + (int)rank;
+            const int sb_row = t.e * trb + t.n0 / 128;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                               a.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb0 = full0 + 8 * stage;
+                const uint32_t sa = smem_base + stage * STAGE, sb = sa + A_BYTES;
+                if (lead) {
                     if (leader)
-                        mbar_expect_tx(fb, 2 * STAGE);
-                    const uint32_t sa = smem_base + stage * STAGE, sb = sa + A_BYTES;
-                    load_2d(&tmA, fb0, sa, kb * (BKB / 2), t.row0 + (int)rank * BM);
-                    load_3d(&tmB, fb0, sb, kb * (BKB / 2), t.n0 + (int)rank * BNH, t.e);
+                        mbar_expect_tx(smem_u32(&aux->full[stage]), 2 * STAGE);
+                    load_2d(&tmA, fb0, sa, kb * (BKB / 2), a_row);
+                    load_3d(&tmB, fb0, sb, kb * (BKB / 2), b_row, t.e);
                     load_2d(&tmSA, fb0, sb + B_BYTES, kb * 256, sa_row);
                     load_2d(&tmSB, fb0, sb + B_BYTES + SFA, kb * 256, sb_row);
-                    ++fills;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                ++fills;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            if (leader)  // the leader's full barriers count both CTAs' bytes
-                for (int s = 0; s < STAGES; ++s) {
-                    const int64_t n = fills / STAGES + (s < fills % STAGES ? 1 : 0);
-                    if (n > 0)
-                        mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
-                }
         }
+        if (leader)  // the leader's full barriers count both CTAs' bytes
+            for (int s = 0; s < STAGES; ++s) {
+                const int64_t n = fills / STAGES + (s < fills % STAGES ? 1 : 0);
+                if (n > 0)
+                    mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
+            }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ---------------------------------------------------------- issuer (leader)
+            const bool lead = elect_one();
             int stage = 0;
             uint32_t phase = 0;
-            int64_t n_st = 0;  // stages issued
-            int ti = 0;        // tiles issued
-            bool ok = true;
+            int old = STAGES - 2;    // the stage issued two before this one, and its phase
+            uint32_t old_phase = 1;
+            uint32_t set = 0;
+            int ti = 0;              // tiles issued
+            bool ok = true, first = true;
             const int nk = (a.K32 + 63) / 64;
+            const uint32_t lo0 = desc_lo(smem_base);
             for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++ti) {
                 // the shared columns of the tile before have been read
                 if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
@@ -734,39 +764,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)((ti & 1) * ACC_STEP);
-                for (int kb = 0; kb < num_kb; ++kb, ++n_st) {
-                    const int set = (int)(n_st & 1);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    // the products of two stages ago are done with this set of scales (before
+                    // the third stage there are none)
                     if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
                                    a.status) ||
-                        (n_st >= 2 && !mbar_wait(smem_u32(&aux->sfree[set]),
-                                                 (uint32_t)(n_st / 2 - 1) & 1u, a.wait_ns,
-                                                 abort_flag, a.status))) {
+                        (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                                              abort_flag, a.status))) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t sa = smem_base + stage * STAGE, sb = sa + A_BYTES;
-                    const uint32_t sfa = sb + B_BYTES, sfb = sfa + SFA;
-                    const uint32_t sf = tmem_base + (uint32_t)(SF_COL + set * kSfCols);
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        sf_copy(sf + hh * 12, sfa + hh * kMx4Tile);
-                        sf_copy(sf + hh * 12 + 4, sfb + hh * kMx4Tile);
-                        sf_copy(sf + hh * 12 + 8, sfb + (2 + hh) * kMx4Tile);
-                    }
-                    const uint64_t da = sdesc(sa), db = sdesc(sb);
+                    const uint32_t la = lo0 + (uint32_t)(stage * (STAGE >> 4));
+                    const uint32_t lb = la + (A_BYTES >> 4);
+                    const uint32_t lsa = lb + (B_BYTES >> 4) - (1u << 16), lsb = lsa + (SFA >> 4);
+                    const uint32_t sf = tmem_base + SF_COL + set;
                     const int ks = min(4, nk - 4 * kb);
+                    if (lead) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k >= ks)
-                            break;
-                        const uint32_t id = (uint32_t)(k & 1) * 2u;
-                        const uint32_t col = sf + (uint32_t)(k >> 1) * 12;
-                        umma(d_tmem, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k),
-                             kIdesc | (id << 4) | (id << 29), col, col + 4, (kb | k) != 0);
+                        for (int hh = 0; hh < 2; ++hh) {
+                            sf_copy(sf + hh * 12, desc(lsa + hh * (kMx4Tile >> 4), kSfDescHi));
+                            sf_copy(sf + hh * 12 + 4, desc(lsb + hh * (kMx4Tile >> 4), kSfDescHi));
+                            sf_copy(sf + hh * 12 + 8, desc(lsb + (2 + hh) * (kMx4Tile >> 4), kSfDescHi));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < ks) {
+                                const uint32_t id = (uint32_t)(k & 1) * 2u;
+                                const uint32_t col = sf + (uint32_t)(k >> 1) * 12;
+                                umma(d_tmem, desc(la + 2 * k, kDescHi), desc(lb + 2 * k, kDescHi),
+                                     kIdesc | (id << 4) | (id << 29), col, col + 4, (kb | k) != 0);
+                            }
+                        commit_both(smem_u32(&aux->empty[stage]));
                     }
-                    commit_both(smem_u32(&aux->empty[stage]));
-                    commit_own(smem_u32(&aux->sfree[set]));
+                    set ^= 32u;
+                    if (++old == STAGES) {
+                        old = 0;
+                        old_phase ^= 1u;
+                        first = false;
+                    }
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -774,9 +809,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 if (!ok)
                     break;
-                commit_both(smem_u32(&aux->tfull[ti & 1]));
+                if (lead)
+                    commit_both(smem_u32(&aux->tfull[ti & 1]));
             }
-            commit_own(smem_u32(&aux->drain));
+            if (lead)
+                commit_own(smem_u32(&aux->drain));
             mbar_drain(smem_u32(&aux->drain), 0);
         }
     } else {
