@@ -261,6 +261,8 @@ EXPERT_CASES = [  # T, E, k, m, d, capacity
     # 4096 rows and more: CTA pairs, one or several column tiles, ragged ends
     (4096, 1, 1, 64, 96, -1), (2100, 3, 2, 200, 320, -1), (1500, 8, 3, 136, 544, 450),
     (2300, 5, 2, 400, 288, -1), (1100, 16, 4, 260, 64, 290),
+    # the second product's K in one to six blocks of 256, and in more
+    (2048, 4, 2, 768, 576, -1), (2100, 2, 2, 1504, 320, -1), (2060, 3, 2, 1568, 160, -1),
 ]
 
 

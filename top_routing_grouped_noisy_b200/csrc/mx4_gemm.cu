@@ -15,7 +15,9 @@
 // one thread run in issue order, so the copies need no wait of their own.
 //
 // Work: tiles of 128 rows x BN columns over every expert, listed on the device from the
-// offsets.  TMEM: two accumulators of BN columns, then the scale columns (24 per set,
+// offsets.  A tile's A rows come in boxes of 32, as many as it has: a TMA box costs the copy
+// engine about 3.5 cycles a 128-byte row whether the row exists or not, and with few rows that
+// bounds the kernel (T = 1: 128-row boxes took 0.38 us a stage).  TMEM: two accumulators of BN columns, then the scale columns (24 per set,
 // four sets).  Roles as in the bf16 kernel: warp 0 TMA producer, warp 1 TMEM allocator
 // and issuer, warps 2-9 epilogue (each thread one row, half of the columns).
 //
@@ -35,6 +37,7 @@ using namespace tc;
 constexpr int BM = 128;
 constexpr int BKB = 128;            // bytes of a stage row: 256 columns
 constexpr int BKC = 256;            // columns of a stage
+constexpr int kABox = 32;           // 1-SM kernel: rows of one A box
 constexpr int ACC = 2;
 constexpr int kSfCols = 24;         // per set: 2 x (4 A + 8 B)
 constexpr int TMEM_COLS = 512;
@@ -311,6 +314,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
             const Tile t = decode_tile<BN>(aux, tile);
+            // rows past the expert's are not loaded: the products read what the stage held, and
+            // only make accumulator rows nobody stores
+            const int a_boxes = min(BM / kABox, (t.row_end - t.row0 + kABox - 1) / kABox);
             const uint8_t *sa_src =
                 a.a_s + (mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM) * tk * kMx4Tile;
             const int nb0 = t.n0 / 128;
@@ -327,8 +333,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t sfa = sb + G::B_BYTES, sfb = sfa + G::SFA;
                 const uint32_t kt = (uint32_t)min(2, tk - 2 * kb) * kMx4Tile;
                 if (lead) {
-                    mbar_expect_tx(fb, (uint32_t)(G::A_BYTES + G::B_BYTES) + kt * (1 + nbt));
-                    tma_load_2d(&tmA, fb, sa, kb * (BKB / 2), t.row0);
+                    mbar_expect_tx(fb, (uint32_t)(a_boxes * kABox * BKB + G::B_BYTES) + kt * (1 + nbt));
+                    for (int i = 0; i < a_boxes; ++i)
+                        tma_load_2d(&tmA, fb, sa + i * kABox * BKB, kb * (BKB / 2), t.row0 + i * kABox);
                     tma_load_3d(&tmB, fb, sb, kb * (BKB / 2), t.n0, t.e);
                     bulk_load(sfa, sa_src + (int64_t)2 * kb * kMx4Tile, kt, fb);
                     for (int i = 0; i < nbt; ++i)
@@ -889,6 +896,360 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 }
 
+// ------------------------------------------------------------------------ resident A
+// The second product has few stages along K (at most kResKb) and, per stage, 256 rows to load
+// for 256 x 256 x 256 of work, which is what bounds it (about 3.3 cycles a 128-byte row and
+// SM).  Here a pair keeps the A rows of its tile, all of K, in shared memory while it walks
+// over a chunk of column tiles, so only B is loaded per stage.  A's K blocks are freed one by
+// one by the chunk's last tile (aempty) and refilled for the next one behind it.
+//   afull[kb]  leader: both CTAs' bytes      aempty[kb]  both CTAs: the leader's commit
+constexpr int kResKb = 6;
+constexpr int RES_STAGE = B_BYTES + SFB;   // 18 KB
+constexpr int RES_A = A_BYTES + SFA;       // one K block of A, 17 KB
+constexpr int kMaxResStages = 7;
+
+struct ResAux {
+    uint64_t full[kMaxResStages];
+    uint64_t empty[kMaxResStages];
+    uint64_t afull[kResKb];
+    uint64_t aempty[kResKb];
+    uint64_t tfull[2];
+    uint64_t tfree;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int32_t off[MOE_MAX_EXPERTS + 1];
+    int32_t ustart[MOE_MAX_EXPERTS + 1];
+    int32_t chunk;
+};
+inline int res_stages(int num_kb)
+{
+    const int left = 227 * 1024 - 1024 - kEpiStageBytes - (int)sizeof(ResAux) - num_kb * RES_A;
+    const int n = left / RES_STAGE;
+    return n < kMaxResStages ? n : kMaxResStages;
+}
+inline int res_smem(int num_kb)
+{
+    return 1024 + kEpiStageBytes + (int)sizeof(ResAux) + num_kb * RES_A + res_stages(num_kb) * RES_STAGE;
+}
+
+// A unit: row tile and chunk of column tiles [n_lo, n_hi) of expert e.
+struct ResUnit {
+    int e, row0, row_end, off, n_lo, n_hi;
+};
+__device__ __forceinline__ ResUnit res_unit(const ResAux *aux, int unit, int n_tiles, int nchunks)
+{
+    ResUnit u;
+    int e = 0;
+    while (unit >= aux->ustart[e + 1])
+        ++e;
+    const int local = unit - aux->ustart[e];
+    const int mt = local / nchunks, c = local - mt * nchunks;
+    u.e = e;
+    u.off = aux->off[e];
+    u.row0 = u.off + mt * 2 * BM;
+    u.row_end = aux->off[e + 1];
+    u.n_lo = c * aux->chunk;
+    u.n_hi = min(n_tiles, u.n_lo + aux->chunk);
+    return u;
+}
+
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    mx4_down_res_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSA,
+                        const __grid_constant__ CUtensorMap tmSB,
+                        const __grid_constant__ CUtensorMap tmO, const __grid_constant__ GemmArgs a,
+                        int stages)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int num_kb = (a.K32 + BKC - 1) / BKC;
+    const int ring = num_kb * RES_A, epi = ring + stages * RES_STAGE;
+    ResAux *aux = reinterpret_cast<ResAux *>(smem + epi + kEpiStageBytes);
+    const int warp = warp_number(), lane = threadIdx.x & 31;
+    volatile int32_t *abort_flag = &aux->abort_flag;
+    const uint32_t rank = cta_rank();
+    const bool leader = rank == 0;
+    const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(smem_u32(&aux->full[s]), 1);
+            mbar_init(smem_u32(&aux->empty[s]), 1);
+        }
+        for (int kb = 0; kb < num_kb; ++kb) {
+            mbar_init(smem_u32(&aux->afull[kb]), 1);
+            mbar_init(smem_u32(&aux->aempty[kb]), 1);
+        }
+        for (int i = 0; i < 2; ++i)
+            mbar_init(smem_u32(&aux->tfull[i]), 1);
+        mbar_init(smem_u32(&aux->tfree), 2 * EPI_WARPS);
+        mbar_init(smem_u32(&aux->drain), 1);
+        aux->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        const CUtensorMap *maps[5] = {&tmA, &tmB, &tmSA, &tmSB, &tmO};
+        for (int i = 0; i < 5; ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(maps[i])) : "memory");
+    }
+    const int n_tiles = (a.N + BN - 1) / BN;
+    if (warp == 2) {
+        for (int i = lane; i <= a.E; i += 32)
+            aux->off[i] = a.offsets[i];
+        __syncwarp();
+        if (lane == 0) {
+            int mt = 0;
+            for (int e = 0; e < a.E; ++e)
+                mt += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM);
+            // column tiles per chunk: the fewest loads on the busiest pair, A counting as much
+            // as one column tile's B
+            int best = 1;
+            int64_t best_cost = INT64_MAX;
+            for (int c = 1; c <= 16; c *= 2) {
+                const int64_t units = (int64_t)mt * ((n_tiles + c - 1) / c);
+                const int64_t cost = (units + nclusters - 1) / nclusters * (min(c, n_tiles) + 1);
+                if (cost < best_cost) {
+                    best_cost = cost;
+                    best = c;
+                }
+            }
+            aux->chunk = best;
+            const int nchunks = (n_tiles + best - 1) / best;
+            int acc = 0;
+            for (int e = 0; e < a.E; ++e) {
+                aux->ustart[e] = acc;
+                acc += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM) * nchunks;
+            }
+            aux->ustart[a.E] = acc;
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&aux->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = aux->tmem_base;
+    const int total = aux->ustart[a.E];
+    const int nchunks = (n_tiles + aux->chunk - 1) / aux->chunk;
+    const int trb = (a.N + 127) / 128;
+    const uint32_t smem_base = smem_u32(smem);
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- TMA producer (both)
+        const bool lead = elect_one();
+        const uint32_t full0 = map_rank(smem_u32(&aux->full[0]), 0);
+        const uint32_t afull0 = map_rank(smem_u32(&aux->afull[0]), 0);
+        int stage = 0, nu = 0;
+        uint32_t phase = 0;
+        int64_t fills = 0;
+        bool ok = true;
+        int a_fills = 0;  // K blocks of A issued
+        for (int unit = cluster_id; unit < total && ok; unit += nclusters, ++nu) {
+            const ResUnit u = res_unit(aux, unit, n_tiles, nchunks);
+            const int a_row = u.row0 + (int)rank * BM;
+            const int sa_row = (int)mx4_expert_tile(u.off, u.e) + (u.row0 - u.off) / BM + (int)rank;
+            for (int nt = u.n_lo; nt < u.n_hi && ok; ++nt) {
+                const int b_row = nt * BN + (int)rank * BNH, sb_row = u.e * trb + nt * (BN / 128);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (nt == u.n_lo) {
+                        if (!mbar_wait(smem_u32(&aux->aempty[kb]), (uint32_t)(nu & 1) ^ 1u, a.wait_ns,
+                                       abort_flag, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lead) {
+                            const uint32_t sa = smem_base + kb * RES_A, fb0 = afull0 + 8 * kb;
+                            if (leader)
+                                mbar_expect_tx(smem_u32(&aux->afull[kb]), 2 * RES_A);
+                            load_2d(&tmA, fb0, sa, kb * (BKB / 2), a_row);
+                            load_2d(&tmSA, fb0, sa + A_BYTES, kb * 256, sa_row);
+                        }
+                        ++a_fills;
+                    }
+                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                                   a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lead) {
+                        const uint32_t sb = smem_base + ring + stage * RES_STAGE, fb0 = full0 + 8 * stage;
+                        if (leader)
+                            mbar_expect_tx(smem_u32(&aux->full[stage]), 2 * RES_STAGE);
+                        load_3d(&tmB, fb0, sb, kb * (BKB / 2), b_row, u.e);
+                        load_2d(&tmSB, fb0, sb + B_BYTES, kb * 256, sb_row);
+                    }
+                    ++fills;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        if (leader) {  // the leader's full barriers count both CTAs' bytes
+            for (int s = 0; s < stages; ++s) {
+                const int64_t n = fills / stages + (s < fills % stages ? 1 : 0);
+                if (n > 0)
+                    mbar_drain(smem_u32(&aux->full[s]), (uint32_t)((n - 1) & 1));
+            }
+            for (int kb = 0; kb < num_kb; ++kb) {
+                const int n = a_fills / num_kb + (kb < a_fills % num_kb ? 1 : 0);
+                if (n > 0)
+                    mbar_drain(smem_u32(&aux->afull[kb]), (uint32_t)((n - 1) & 1));
+            }
+        }
+    } else if (warp == 1) {
+        if (leader) {
+            // ---------------------------------------------------------- issuer (leader)
+            const bool lead = elect_one();
+            int stage = 0, nu = 0;
+            uint32_t phase = 0;
+            int old = stages - 2;    // the stage issued two before this one, and its phase
+            uint32_t old_phase = 1;
+            uint32_t set = 0;
+            int ti = 0;              // tiles issued
+            bool ok = true, first = true;
+            const int nk = (a.K32 + 63) / 64;
+            const uint32_t lo0 = desc_lo(smem_base);
+            for (int unit = cluster_id; unit < total && ok; unit += nclusters, ++nu) {
+                const ResUnit u = res_unit(aux, unit, n_tiles, nchunks);
+                for (int nt = u.n_lo; nt < u.n_hi && ok; ++nt, ++ti) {
+                    // the shared columns of the tile before have been read
+                    if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                                             abort_flag, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + (uint32_t)((ti & 1) * ACC_STEP);
+                    for (int kb = 0; kb < num_kb; ++kb) {
+                        // with the products of two stages ago done this set of scales is free
+                        if ((nt == u.n_lo && !mbar_wait(smem_u32(&aux->afull[kb]), (uint32_t)nu & 1u,
+                                                        a.wait_ns, abort_flag, a.status)) ||
+                            !mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                                       a.status) ||
+                            (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                                                  abort_flag, a.status))) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t la = lo0 + (uint32_t)(kb * (RES_A >> 4));
+                        const uint32_t lb = lo0 + (uint32_t)((ring + stage * RES_STAGE) >> 4);
+                        const uint32_t lsa = la + (A_BYTES >> 4) - (1u << 16);
+                        const uint32_t lsb = lb + (B_BYTES >> 4) - (1u << 16);
+                        const uint32_t sf = tmem_base + SF_COL + set;
+                        const int ks = min(4, nk - 4 * kb);
+                        if (lead) {
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                sf_copy(sf + hh * 12, desc(lsa + hh * (kMx4Tile >> 4), kSfDescHi));
+                                sf_copy(sf + hh * 12 + 4, desc(lsb + hh * (kMx4Tile >> 4), kSfDescHi));
+                                sf_copy(sf + hh * 12 + 8, desc(lsb + (2 + hh) * (kMx4Tile >> 4), kSfDescHi));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < ks) {
+                                    const uint32_t id = (uint32_t)(k & 1) * 2u;
+                                    const uint32_t col = sf + (uint32_t)(k >> 1) * 12;
+                                    umma(d_tmem, desc(la + 2 * k, kDescHi), desc(lb + 2 * k, kDescHi),
+                                         kIdesc | (id << 4) | (id << 29), col, col + 4, (kb | k) != 0);
+                                }
+                            commit_both(smem_u32(&aux->empty[stage]));
+                            if (nt + 1 == u.n_hi)
+                                commit_both(smem_u32(&aux->aempty[kb]));
+                        }
+                        set ^= 32u;
+                        if (++old == stages) {
+                            old = 0;
+                            old_phase ^= 1u;
+                            first = false;
+                        }
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    if (lead)
+                        commit_both(smem_u32(&aux->tfull[ti & 1]));
+                }
+            }
+            if (lead)
+                commit_own(smem_u32(&aux->drain));
+            mbar_drain(smem_u32(&aux->drain), 0);
+        }
+    } else {
+        // -------------------------------------------------------------- epilogue (both)
+        const int lane_base = (warp & 3) * 32;
+        const int half = (warp - 2) / 4;  // 64-column groups 2 half, 2 half + 1
+        const uint32_t tfree0 = map_rank(smem_u32(&aux->tfree), 0);
+        EpiStore st{&tmO, smem_base + (uint32_t)(epi + (warp - 2) * 2 * kStageSlotBytes), 0};
+        int ti = 0;
+        bool ok = true;
+        for (int unit = cluster_id; unit < total && ok; unit += nclusters) {
+            const ResUnit u = res_unit(aux, unit, n_tiles, nchunks);
+            const int row0 = u.row0 + (int)rank * BM + lane_base, row = row0 + lane;
+            for (int nt = u.n_lo; nt < u.n_hi; ++nt, ++ti) {
+                const int acc = ti & 1;
+                if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+                               a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr =
+                    tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * ACC_STEP);
+                const bool shares = half == 1 - acc;  // as in the kernel above
+                if (!shares && lane == 0)
+                    mbar_arrive_cluster(tfree0);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
+                    uint32_t v[2][32];
+                    tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
+                    tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
+                    tmem_wait_ld();
+                    if (shares && i == 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(tfree0);
+                    }
+                    store_64(a, v, nt * BN + gi * 64, row0, row, u.row_end, st);
+                    __syncwarp();  // the next tcgen05.ld takes the whole warp
+                }
+            }
+        }
+        if (lane == 0)
+            bulk_wait_all();  // this lane's output stores are done before the CTA exits
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (threadIdx.x == 0) {  // after an abort, as in the kernel above
+        const int peer_abort = ld_cluster_s32(map_rank(smem_u32(&aux->abort_flag), rank ^ 1u));
+        if (*abort_flag || peer_abort) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kAbortSettleNs) {
+            }
+        }
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
 }  // namespace pair
 
 // ------------------------------------------------------------------------ host side
@@ -950,7 +1311,8 @@ static cudaError_t prepare_device(DevInfo **out)
             (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_UP>, pair::smem_bytes<EPI_UP>())) !=
                 cudaSuccess ||
             (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_DOWN>, pair::smem_bytes<EPI_DOWN>())) !=
-                cudaSuccess)
+                cudaSuccess ||
+            (e = allow_smem(pair::mx4_down_res_kernel, 227 * 1024)) != cudaSuccess)
             return e;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
@@ -1024,7 +1386,7 @@ static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const
     const uint64_t da[2] = {kel, (uint64_t)rows}, sa[1] = {pitch};
     const uint64_t db[3] = {kel, (uint64_t)args.N, (uint64_t)args.E};
     const uint64_t sb[2] = {pitch, pitch * args.N};
-    const uint32_t ba[2] = {BKB / 2, BM}, bb[3] = {BKB / 2, (uint32_t)(two ? pair::BNH : bn), 1};
+    const uint32_t ba[2] = {BKB / 2, (uint32_t)(two ? BM : kABox)}, bb[3] = {BKB / 2, (uint32_t)(two ? pair::BNH : bn), 1};
     if ((e = make_map(&ta, A, 2, da, sa, ba)) != cudaSuccess ||
         (e = make_map(&tb, B, 3, db, sb, bb)) != cudaSuccess)
         return e;
@@ -1048,6 +1410,12 @@ static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const
         return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
+    const int num_kb = (args.K32 + BKC - 1) / BKC;
+    if (EPI == EPI_DOWN && num_kb <= pair::kResKb) {
+        cluster_config(&cfg, attr, di->pair_clusters, pair::res_smem(num_kb), s);
+        return cudaLaunchKernelEx(&cfg, pair::mx4_down_res_kernel, ta, tb, tsa, tsb, to, args,
+                                  pair::res_stages(num_kb));
+    }
     cluster_config(&cfg, attr, di->pair_clusters, pair::smem_bytes<EPI>(), s);
     const int band_rows = gemm_band_rows();
     const int band = band_rows <= 0 ? 0 : (band_rows + 2 * BM - 1) / (2 * BM);
