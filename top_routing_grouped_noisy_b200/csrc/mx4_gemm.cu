@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int nbt = min(G::BT, trb - nb0);  // B scale tiles that exist
             const uint8_t *sb_src = a.b_s + ((int64_t)t.e * trb + nb0) * tk * kMx4Tile;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const Tile t = decode_tile<BN>(aux, tile);
             // first B scale column inside the copied tiles: one column per 32 rows
             const uint32_t b_shift = (uint32_t)(t.n0 % 128 / 32);
-            if (!mbar_wait(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
+            if (!mbar_wait_spin(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
                            a.status)) {
                 ok = false;
                 break;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag, a.status)) {
+                if (!mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = decode_tile<BN>(aux, tile);
-            if (!mbar_wait(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
+            if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
                 break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
@@ -556,9 +556,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
+// Relaxed: what the arrival hands over is accumulator columns, ordered by tcgen05.wait::ld and
+// the tcgen05 fences.  A release would first wait for this thread's stores of h or of the
+// last output tile, about 700 ns in which no products run.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
 __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t cluster_addr)
@@ -614,6 +617,18 @@ __device__ __forceinline__ void commit_own(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                      bar)
                  : "memory");
+}
+
+// Epilogue warps w and w + 4 read the same TMEM lanes, one at a time: the warp without shared
+// columns lets the other's first load pass (taken in any order, the next tile's products start
+// about 900 cycles later).  Named barriers 1..4, one for each quarter of the lanes.
+__device__ __forceinline__ void pair_go(int warp)
+{
+    asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+}
+__device__ __forceinline__ void pair_wait(int warp)
+{
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
 }
 
 // Tile order inside an expert: bands of `band` row tiles, row tiles fastest inside a band,
@@ -721,7 +736,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int sa_row = (int)mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM + (int)rank;
             const int sb_row = t.e * trb + t.n0 / 128;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t lo0 = desc_lo(smem_base);
             for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++ti) {
                 // the shared columns of the tile before have been read
-                if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                if (ti > 0 && !mbar_wait_spin(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
                                          abort_flag, a.status)) {
                     ok = false;
                     break;
@@ -774,9 +789,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int kb = 0; kb < num_kb; ++kb) {
                     // the products of two stages ago are done with this set of scales (before
                     // the third stage there are none)
-                    if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                    if (!mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
                                    a.status) ||
-                        (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                        (!first && !mbar_wait_spin(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
                                               abort_flag, a.status))) {
                         ok = false;
                         break;
@@ -833,7 +848,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int tile = cluster_id; tile < total; tile += nclusters, ++ti) {
             const Tile t = decode(aux, tile, n_tiles, band);
             const int acc = ti & 1;
-            if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+            if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                            a.status))
                 break;
             tc_fence_after();
@@ -849,6 +864,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
                 uint32_t v[2][32];
+                if (!shares && i == 0)
+                    pair_wait(warp);
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                 tmem_wait_ld();
@@ -857,6 +874,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(tfree0);
+                    pair_go(warp);
                 }
                 if constexpr (EPI == EPI_UP) {
                     const int nb = t.n0 / 2 + gi * 32;  // 32 neurons: one block of h
@@ -1059,7 +1077,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int b_row = nt * BN + (int)rank * BNH, sb_row = u.e * trb + nt * (BN / 128);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (nt == u.n_lo) {
-                        if (!mbar_wait(smem_u32(&aux->aempty[kb]), (uint32_t)(nu & 1) ^ 1u, a.wait_ns,
+                        if (!mbar_wait_spin(smem_u32(&aux->aempty[kb]), (uint32_t)(nu & 1) ^ 1u, a.wait_ns,
                                        abort_flag, a.status)) {
                             ok = false;
                             break;
@@ -1073,7 +1091,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                         ++a_fills;
                     }
-                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                    if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                    a.status)) {
                         ok = false;
                         break;
@@ -1122,7 +1140,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const ResUnit u = res_unit(aux, unit, n_tiles, nchunks);
                 for (int nt = u.n_lo; nt < u.n_hi && ok; ++nt, ++ti) {
                     // the shared columns of the tile before have been read
-                    if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                    if (ti > 0 && !mbar_wait_spin(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
                                              abort_flag, a.status)) {
                         ok = false;
                         break;
@@ -1131,11 +1149,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t d_tmem = tmem_base + (uint32_t)((ti & 1) * ACC_STEP);
                     for (int kb = 0; kb < num_kb; ++kb) {
                         // with the products of two stages ago done this set of scales is free
-                        if ((nt == u.n_lo && !mbar_wait(smem_u32(&aux->afull[kb]), (uint32_t)nu & 1u,
+                        if ((nt == u.n_lo && !mbar_wait_spin(smem_u32(&aux->afull[kb]), (uint32_t)nu & 1u,
                                                         a.wait_ns, abort_flag, a.status)) ||
-                            !mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                            !mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
                                        a.status) ||
-                            (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                            (!first && !mbar_wait_spin(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
                                                   abort_flag, a.status))) {
                             ok = false;
                             break;
@@ -1199,7 +1217,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int row0 = u.row0 + (int)rank * BM + lane_base, row = row0 + lane;
             for (int nt = u.n_lo; nt < u.n_hi; ++nt, ++ti) {
                 const int acc = ti & 1;
-                if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -1214,6 +1232,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int i = 0; i < 2; ++i) {
                     const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
                     uint32_t v[2][32];
+                    if (!shares && i == 0)
+                        pair_wait(warp);
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                     tmem_wait_ld();
@@ -1222,6 +1242,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive_cluster(tfree0);
+                        pair_go(warp);
                     }
                     store_64(a, v, nt * BN + gi * 64, row0, row, u.row_end, st);
                     __syncwarp();  // the next tcgen05.ld takes the whole warp
