@@ -31,6 +31,8 @@ constexpr int kWsDecodeBarrierWord = 4;
 constexpr int kWsFrontBarrierWord = 6;
 // Header bytes that clearing the status resets (status word and counters).
 constexpr size_t kWsResetBytes = 32;
+// Words 16-17: grid barrier of the mx4 few-token kernel (64-bit count of arrivals, never reset).
+constexpr int kWsMx4BarrierWord = 16;
 // Words 8-9: offsets {0, T} of the shared block's one-expert GEMMs (residual MoE).
 constexpr int kWsTokenRangeWord = 8;
 

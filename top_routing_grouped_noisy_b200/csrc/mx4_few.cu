@@ -27,15 +27,14 @@
 // k indexes are 8 consecutive columns, for A and B alike (the order of k inside a product
 // is free).
 //
-// Weights stream through a ring of stages (GEMM 1: 16 rows x 256 columns, GEMM 2: 32 x 128,
-// with their 32 scale words) that each warp fills for itself with cp.async, several stages
-// ahead and across items: no barrier between loads and products but __syncwarp.  The loop is
-// bound by the integer pipe (the conversions) and by shared-memory wavefronts, which is why B
-// stays in registers in GEMM 1 and serves 32 rows in GEMM 2.  Partial sums meet in shared
-// memory in warp order, so results do not depend on timing.
-//
-// Rows are enumerated in the order of the scale tiles (4 rows that lie 32 apart share 16
-// bytes of scales), so that the scale words of an item fill whole sectors.
+// Weights stream through two stages of 32 rows x 256 columns with their 64 scale words, which
+// each warp fills for itself with cp.async, one stage ahead and across items: no barrier
+// between loads and products but __syncwarp.  The loop is bound by the integer pipe (the
+// conversions) and by the load unit's lines and wavefronts: B stays in registers (it never
+// passes through shared memory), a copy instruction covers whole 128-byte lines of 4 rows, and
+// rows are enumerated in the order of the scale tiles -- 4 rows that lie 32 apart share 16
+// bytes of scales -- so that one copy instruction brings all scales of a stage.  Partial sums
+// meet in shared memory in warp order, so results do not depend on timing.
 #include <mutex>
 #include <type_traits>
 
@@ -49,7 +48,6 @@ namespace few {
 using tc::smem_u32;
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kChunkCols = 128;
 constexpr int kChunkBytes = 16 * 64 + 64;     // 16 rows x 128 columns: codes, scale words
 constexpr int kSlice = 256;                   // columns of a stage
 constexpr int kStageBytes = 4 * kChunkBytes;  // 32 rows x 256 columns: [16 rows][128 columns]
@@ -58,9 +56,8 @@ constexpr int kWindow1 = kWarps * kSlice;     // columns of x at a time
 constexpr int kStrip = 32;                    // GEMM 2: output columns at a time
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
-constexpr int kRegion = 72 * 1024;            // the warps' sums, or staged rows of h
-constexpr int kMaxInv = 1088;                 // (row, chunk) scales of a window of h
-constexpr int kSmem = kRegion + kRingBytes;   // dynamic; the static tables take 15 KB
+constexpr int kRegion = 72 * 1024;            // the warps' sums
+constexpr int kSmem = kRegion + kRingBytes;   // dynamic; the static tables take 10 KB
 
 struct Args {
     const bf16 *x, *Wg, *Wn;
@@ -69,26 +66,20 @@ struct Args {
     bf16 *h, *y;
     float *loss, *importance, *f, *P, *probs_sum, *w;
     int32_t *counts, *idx, *row_token, *slot_row, *kept, *offsets;
-    int32_t *status, *gbar;
+    int32_t *status;
+    unsigned long long *gbar;  // arrivals at the grid barrier, ever
     uint64_t wait_ns;
     float lambda, scale;
     int T, d, m, E, k, C, router_type;
-    int win2;          // columns of h staged at once
     int tk1, tk2;      // tiles of a scale tile row of W13, W2
     int64_t w13_codes, w13_scales, w2_codes, w2_scales;  // bytes of one expert
 };
 
-// 16 or 4 bytes to shared memory; zeros where `on` is false (nothing is read then)
+// 16 bytes to shared memory; zeros where `on` is false (nothing is read then)
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(on ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void *src, bool on)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(on ? 4 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -102,12 +93,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr)
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
+__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long *p)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&b)[4])
@@ -134,10 +123,6 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-
-// pitch (bytes) of staged rows of n columns: 64 mod 128, so that the fragment loads of
-// two neighbouring rows fall into different banks
-__host__ __device__ inline int row_pitch(int n) { return (2 * n + 127) / 128 * 128 + 64; }
 
 // --------------------------------------------------------------------- work items
 // GEMM 1 works on quads of neurons (4 that share 16 bytes of scales), 16 quads per 64
@@ -248,140 +233,124 @@ struct UpWalk {
     }
 };
 
-// A lane's place in a stage: row (lane / 4) of a 16-row chunk, 16-byte piece lane % 4
-__device__ __forceinline__ uint32_t stage_place()
-{
-    const int lane = threadIdx.x & 31, row = lane >> 2, piece = lane & 3;
-    return (uint32_t)(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-}
+// A lane's place in a stage.  A copy instruction brings 128-byte lines (256 columns) of the 4
+// rows of a quad: lane l has row l / 8 of it and 16-byte piece l % 8, which belongs to 128-
+// column chunk l / 4 % 2.  Rows lie 64 bytes apart in a chunk, their 4 pieces swizzled by
+// (row / 2) % 4; quads 2 j and 2 j + 1 of 8 rows differ in that swizzle.
+struct Place {
+    uint32_t quad[2];
+    __device__ __forceinline__ Place()
+    {
+        const int lane = threadIdx.x & 31, row = lane >> 3, piece = lane & 3;
+        const uint32_t u = (uint32_t)((lane >> 2 & 1) * kChunkBytes + row * 64);
+        quad[0] = u + (uint32_t)((piece ^ (row >> 1)) << 4);
+        quad[1] = u + (uint32_t)(256 + ((piece ^ (2 + (row >> 1))) << 4));
+    }
+    // quad i of a 32-row stage: chunks [16 rows][128 columns], 4 quads of 4 rows each
+    __device__ __forceinline__ uint32_t at(int i) const
+    {
+        return (uint32_t)((i >> 2) * 2 * kChunkBytes + (i >> 1 & 1) * 512) + quad[i & 1];
+    }
+};
 
 // Fills a stage of GEMM 1 (one group of copies): the item's 16 neurons, W1 rows of the first 8
-// and their W3 rows, then the other 8, x the 256 columns from col on.  Neuron s of an item
-// that starts at quad q lies at W13 row 128 (qq / 16) + 32 (s % 4) + qq % 16 with qq = q +
-// s / 4, its W3 row 16 further; the scale words at 16 (qq % 16 [+ 16]) + 4 (s % 4) of tile
-// qq / 16.  Rows past the expert's and columns past d become zeros.
-__device__ __forceinline__ void up_fill(const Args &a, int32_t item, int col, uint32_t st)
+// and their W3 rows, then the other 8, x the 256 columns from col on.  Quad qq is W13 rows
+// 128 (qq / 16) + qq % 16 + 32 i, its W3 rows 16 further; their scale words are 16 bytes at
+// 16 (qq % 16 [+ 16]) of tile qq / 16.  Rows past the expert's and columns past d become zeros.
+__device__ __forceinline__ void up_fill(const Args &a, int32_t item, int col, uint32_t st,
+                                        const Place &place)
 {
-    const int lane = threadIdx.x & 31;
-    const int e = item_expert(item), n4 = 4 * item_quads(item), q = item_first(item);
-    const int half = a.d >> 1, at = (col >> 1) + (lane & 3) * 16;
-    const uint8_t *ce = a.W13q + e * a.w13_codes + at;
-    const bool in0 = at < half, in1 = at + 64 < half;
-    st += stage_place();
+    const int lane = threadIdx.x & 31, r = lane >> 3;
+    const int e = item_expert(item), n = item_quads(item), q = item_first(item);
+    const int half = a.d >> 1, at = (col >> 1) + (lane & 7) * 16;
+    const uint8_t *ce = a.W13q + e * a.w13_codes + (int64_t)(32 * r) * half + at;
+    const bool in = at < half;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int s = 8 * h + (lane >> 2), qq = q + (s >> 2), t = (qq >> 4) * 64 + (qq & 15);
-        const bool on = s < n4 && t + 16 * (s & 3) < a.m;
-        const uint8_t *s0 = ce + (int64_t)((qq >> 4) * 128 + 32 * (s & 3) + (qq & 15)) * half;
-        const uint8_t *s1 = s0 + 16 * half;
-        cp16(st + 2 * h * kChunkBytes, s0, on && in0);
-        cp16(st + 2 * h * kChunkBytes + 512, s1, on && in0);
-        cp16(st + (2 * h + 1) * kChunkBytes, s0 + 64, on && in1);
-        cp16(st + (2 * h + 1) * kChunkBytes + 512, s1 + 64, on && in1);
+    for (int j = 0; j < 4; ++j) {
+        const int qq = q + j;
+        const bool on = in && j < n && (qq >> 4) * 64 + (qq & 15) + 16 * r < a.m;
+        const uint8_t *s0 = ce + (int64_t)((qq >> 4) * 128 + (qq & 15)) * half;
+        cp16(st + place.at((j >> 1) * 4 + (j & 1)), s0, on);
+        cp16(st + place.at((j >> 1) * 4 + 2 + (j & 1)), s0 + 16 * half, on);
     }
-    // scale words: lane % 16 the row of the chunk, lane / 16 the chunk
-    const int ch = (col >> 7) + (lane >> 4);
-    const uint8_t *se = a.W13s + e * a.w13_scales + (lane & 8) * 32 + (int64_t)ch * kMx4Tile;
-    st += (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4 - stage_place();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int s = 8 * h + (lane & 7), qq = q + (s >> 2);
-        const bool on = s < n4 && (qq >> 4) * 64 + (qq & 15) + 16 * (s & 3) < a.m && ch < a.tk1;
-        cp4(st + 2 * h * kChunkBytes,
-            se + (int64_t)((qq >> 4) * a.tk1) * kMx4Tile + (qq & 15) * 16 + (s & 3) * 4, on);
+    // scales: lane = (chunk, W1 or W3, quad)
+    if (lane < 16) {
+        const int j = lane & 3, up = lane >> 2 & 1, u = lane >> 3, qq = q + j, ch = (col >> 7) + u;
+        cp16(st + (uint32_t)((2 * (j >> 1) + u) * kChunkBytes + 1024 + up * 32 + (j & 1) * 16),
+             a.W13s + e * a.w13_scales + ((int64_t)((qq >> 4) * a.tk1) + ch) * kMx4Tile +
+                 ((qq & 15) + 16 * up) * 16,
+             j < n && ch < a.tk1);
     }
     cp_commit();
 }
 
-// How GEMM 2 is shared out: the (selected expert, 256 columns of h) pairs of a window go
-// round the warps.
+// How GEMM 2 is shared out: the (selected expert, 256 columns of h) pairs go round the warps.
 struct DownPlan {
-    int lo, hi, strips, nsel, half, win, n_win;  // win: columns
+    int lo, hi, strips, nsel, units;  // units: of an expert
     __device__ __forceinline__ DownPlan(const Args &a, int sel)
     {
         const uint32_t all = (uint32_t)((a.d + 127) / 128 * 32);
         lo = (int)(blockIdx.x * all / gridDim.x);
         hi = (int)((blockIdx.x + 1) * all / gridDim.x);
-        strips = sel == 0 ? 0 : (4 * (hi - lo) + kStrip - 1) / kStrip;
+        strips = (4 * (hi - lo) + kStrip - 1) / kStrip;
         nsel = sel;
-        half = mx4_k32(a.m) >> 1;
-        win = a.win2;
-        n_win = (2 * half + win - 1) / win;
-    }
-    __device__ __forceinline__ int units(int w) const
-    {
-        return (min(win, 2 * half - w * win) + kSlice - 1) / kSlice;
+        units = (a.m + kSlice - 1) / kSlice;
     }
 };
-// A warp's way: strips, windows, its pairs (is: expert among the selected, u: unit).
+// A warp's way: strips, its pairs (is: expert among the selected, u: unit).
 struct DownWalk {
-    int strip, w, n, is, u;
-    __device__ __forceinline__ DownWalk(const DownPlan &p) : strip(0), w(0) { open(p); }
+    int strip, is, u;
+    __device__ __forceinline__ DownWalk(const DownPlan &p)
+    {
+        strip = p.nsel == 0 ? p.strips : 0;
+        first(p);
+    }
     __device__ __forceinline__ bool on(const DownPlan &p) const { return strip < p.strips; }
-    __device__ __forceinline__ void open(const DownPlan &p)
+    __device__ __forceinline__ void first(const DownPlan &p)
     {
-        while (strip < p.strips) {
-            n = p.units(w);
-            is = 0;
-            u = (int)threadIdx.x >> 5;
-            wrap();
-            if (is < p.nsel)
-                return;
-            leave(p);
-        }
+        is = 0;
+        u = (int)threadIdx.x >> 5;
+        wrap(p);
+        if (is >= p.nsel)  // no pair for this warp
+            strip = p.strips;
     }
-    __device__ __forceinline__ void wrap()
+    __device__ __forceinline__ void wrap(const DownPlan &p)
     {
-        while (u >= n) {
-            u -= n;
+        while (u >= p.units) {
+            u -= p.units;
             ++is;
-        }
-    }
-    __device__ __forceinline__ void leave(const DownPlan &p)
-    {
-        if (++w == p.n_win) {
-            w = 0;
-            ++strip;
         }
     }
     __device__ __forceinline__ void next(const DownPlan &p)
     {
         u += kWarps;
-        wrap();
+        wrap(p);
         if (__builtin_expect(is >= p.nsel, 0)) {
-            leave(p);
-            open(p);
+            ++strip;
+            first(p);
         }
     }
 };
 
-// Fills a stage of GEMM 2 (one group of copies): the strip's 32 rows of expert e's W2 x the
-// 256 columns from col on; rows past the strip and columns past K32 become zeros.
+// Fills a stage of GEMM 2 (one group of copies): the strip's 8 quads of W2 rows of expert e x
+// the 256 columns from col on; rows past the strip and columns past K32 become zeros.
 __device__ __forceinline__ void down_fill(const Args &a, const DownPlan &p, int strip, int e, int col,
-                                          uint32_t st)
+                                          uint32_t st, const Place &place)
 {
-    const int lane = threadIdx.x & 31, q = p.lo + 8 * strip, rows = 4 * (p.hi - q);
-    const int at = (col >> 1) + (lane & 3) * 16;
-    const uint8_t *ce = a.W2q + e * a.w2_codes + at;
-    const bool in0 = at < p.half, in1 = at + 64 < p.half;
-    st += stage_place();
+    const int lane = threadIdx.x & 31, r = lane >> 3, q = p.lo + 8 * strip, n = p.hi - q;
+    const int half = mx4_k32(a.m) >> 1, at = (col >> 1) + (lane & 7) * 16;
+    const uint8_t *ce = a.W2q + e * a.w2_codes + (int64_t)(32 * r) * half + at;
+    const bool in = at < half;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 2) + 8 * i, row = down_column(q, r);
-        const bool on = r < rows && row < a.d;
-        const uint8_t *s0 = ce + (int64_t)row * p.half;
-        cp16(st + (i >> 1) * 2 * kChunkBytes + (i & 1) * 512, s0, on && in0);
-        cp16(st + ((i >> 1) * 2 + 1) * kChunkBytes + (i & 1) * 512, s0 + 64, on && in1);
+    for (int i = 0; i < 8; ++i) {
+        const int qq = q + i, row = (qq >> 5) * 128 + (qq & 31);
+        cp16(st + place.at(i), ce + (int64_t)row * half, in && i < n && row + 32 * r < a.d);
     }
-    const int ch = (col >> 7) + (lane >> 4);
-    const uint8_t *se = a.W2s + e * a.w2_scales + (int64_t)ch * kMx4Tile;
-    st += (lane >> 4) * kChunkBytes + 1024 + (lane & 15) * 4 - stage_place();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = 16 * h + (lane & 15), row = down_column(q, r);
-        cp4(st + 2 * h * kChunkBytes,
-            se + (int64_t)((row >> 7) * a.tk2) * kMx4Tile + (row & 31) * 16 + (row >> 5 & 3) * 4,
-            r < rows && row < a.d && ch < a.tk2);
+    if (lane < 16) {  // scales: lane = (chunk, quad)
+        const int i = lane & 7, u = lane >> 3, qq = q + i, ch = (col >> 7) + u;
+        cp16(st + (uint32_t)((2 * (i >> 2) + u) * kChunkBytes + 1024 + (i & 3) * 16),
+             a.W2s + e * a.w2_scales + ((int64_t)((qq >> 5) * a.tk2) + ch) * kMx4Tile + (qq & 31) * 16,
+             i < n && (qq >> 5) * 128 < a.d && ch < a.tk2);
     }
     cp_commit();
 }
@@ -415,20 +384,47 @@ __device__ __forceinline__ void to_half(uint4 &v, float mul)
     v = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// GEMM 1's B: columns [col, col + 256) of every token as scaled f16 (lane (g, c): tokens g and
-// g + 8, 8 columns of each of the 8 blocks) and the scales' inverses of tokens 2c, 2c + 1.
-template <int NB>
-__device__ __forceinline__ void load_slice(const Args &a, int col, uint4 (&xb)[NB][8],
-                                           float (&inv)[NB][2][2])
+// B of a stage in registers, as stored: columns [col, col + 256) of the rows at src[nb] (this
+// lane's row of each group of 8 tokens, nullptr: zeros), 8 columns of each of the 8 blocks;
+// columns from `limit` on are zeros.  CG: rows that other SMs wrote in this launch.
+template <int NB, bool CG>
+__device__ __forceinline__ void load_b(const bf16 *const (&src)[NB], int col, int limit,
+                                       uint4 (&xb)[NB][8])
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int c = threadIdx.x & 3;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int t = nb * 8 + g;
-        const bf16 *src = a.x + (int64_t)t * a.d + col + 8 * c;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-            xb[nb][b] = (t < a.T && col + 32 * b < a.d) ? ld_nc(src + 32 * b) : make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < 8; ++b) {
+            const int at = col + 32 * b + 8 * c;
+            xb[nb][b] = make_uint4(0, 0, 0, 0);
+            if (src[nb] != nullptr && at < limit)
+                xb[nb][b] = CG ? __ldcg(reinterpret_cast<const uint4 *>(src[nb] + at)) : ld_nc(src[nb] + at);
+        }
+}
+
+// Turns them into scaled f16; inv[nb][u][j]: weight of token 2c + j's row (w[nb] of the lane
+// that holds it) times the inverse of its scale in chunk u.  limit: as above (the 8 columns
+// around it come with whatever lies behind them).
+template <int NB>
+__device__ __forceinline__ void scale_b(uint4 (&xb)[NB][8], int col, int limit, const float (&w)[NB],
+                                        float (&inv)[NB][2][2])
+{
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    if (col + kSlice > limit && (limit & 7) != 0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const int n = limit - (col + 32 * b + 8 * c);  // columns that exist
+                if (n > 0 && n < 8) {
+                    uint32_t v[4] = {xb[nb][b].x, xb[nb][b].y, xb[nb][b].z, xb[nb][b].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = 2 * i + 1 < n ? v[i] : (2 * i < n ? v[i] & 0xffffu : 0u);
+                    xb[nb][b] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -444,59 +440,11 @@ __device__ __forceinline__ void load_slice(const Args &a, int col, uint4 (&xb)[N
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 to_half(xb[nb][4 * u + b], __uint_as_float(field << 23));
-            const float r = mx4_scale(254u - field);
+            const float r = mx4_scale(254u - field) * w[nb];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 inv[nb][u][j] = __shfl_sync(0xffffffffu, r, (2 * c + j) * 4);
         }
-}
-
-// Stages rows [0, n), `chunks` chunks from column c0 (row j at src + j ld, columns below
-// `valid` exist, zeros past them) as scaled f16; inv[j * chunks + ch]: the scales' inverses
-// times weight[j].  Called by the whole CTA, each half warp one chunk of one row at a time.
-__device__ __forceinline__ void stage_rows(char *region, int pitch, float *inv, int n, int c0,
-                                           int chunks, int valid, const bf16 *src, int64_t ld,
-                                           const float *weight)
-{
-    const int total = n * chunks;
-    const int hw = (int)threadIdx.x >> 4, l = threadIdx.x & 15;
-    constexpr int U = 4, step = 2 * kWarps;
-#pragma unroll 1
-    for (int i0 = hw & ~1; i0 < total; i0 += U * step) {  // both halves of a warp loop alike
-        uint4 v[U];
-        int at[U], row[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + (hw & 1) + u * step;
-            const int j = i / chunks, col = (i - j * chunks) * kChunkCols + 8 * l;
-            at[u] = i < total ? j * pitch + col * 2 : -1;
-            row[u] = j;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (i < total && c0 + col < valid)
-                v[u] = __ldcg(reinterpret_cast<const uint4 *>(src + j * ld + c0 + col));
-            if (c0 + col + 8 > valid) {  // columns past the row's end hold anything
-                uint16_t *e = reinterpret_cast<uint16_t *>(&v[u]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c0 + col + q >= valid)
-                        e[q] = 0;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            uint32_t top = top_of(v[u]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t field = scale_field(top);
-            to_half(v[u], __uint_as_float(field << 23));
-            if (at[u] >= 0) {
-                st_v4(region + at[u], v[u]);
-                if (l == 0)
-                    inv[i0 + (hw & 1) + u * step] = mx4_scale(254u - field) * weight[row[u]];
-            }
-        }
-    }
 }
 
 // 2^s of the four bytes of a scale word (0: 2^-127, 255: NaN, as the conversion has them)
@@ -545,83 +493,92 @@ __device__ __forceinline__ void chunk_mma(float (&sum)[NB][4], uint32_t st, cons
 }
 
 // --------------------------------------------------------------------- the router
-// The logits lg [T][nout] of all tokens: warp w takes the 32-column steps [w S / 16,
-// (w + 1) S / 16), eight at a time, with its rows of [W_g | W_noise] in its own `stage`
-// bytes; the warps' sums (`part`) are added in warp order.
-template <int NT>
-__device__ __noinline__ void router_logits(const Args &a, char *stage, int stage_bytes, float *part,
-                                           float *lg)
+// The logits lg [T][nout] of all tokens.  A group's warps have the slices of a window of x in
+// registers already (x, of window 0; left holding the last window's); the groups share a
+// slice's 32-column steps, step s to group s % groups.  The warp's rows of [W_g | W_noise] pass through its own `stage` bytes, and
+// the warps' sums (`part`) are added in warp order.
+template <int NB>
+__device__ __forceinline__ void router_logits(const Args &a, const UpPlan &p, uint4 (&x)[NB][8],
+                                              char *stage, int stage_bytes, float *part, float *lg)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int E = a.E, T = a.T, d = a.d, nout = a.Wn != nullptr ? 2 * E : E;
-    constexpr int NP = NT * 8;
-    const int round = min(8, stage_bytes / (32 * NP * 2));
+    const int NT = (nout + 7) / 8, NP = NT * 8;
+    const int room = stage_bytes / (64 * NP), grp = p.group(), gshift = 4 - p.kshift;
     const uint32_t sb = smem_u32(stage);
-    const int steps = d / 32, s_hi = (warp + 1) * steps / kWarps;
-    float acc[NT][4];
+    float acc[4][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             acc[nt][q] = 0.f;
 #pragma unroll 1
-    for (int s0 = warp * steps / kWarps; s0 < s_hi; s0 += round) {
-        const int n = min(round, s_hi - s0);
-        const int64_t k0 = s0 * 32;
-        __syncwarp();
-        if ((E & 7) == 0) {  // rows of whole 16-byte pieces
+    for (int w = 0; w < p.n_win; ++w) {
+        const int col = p.column(w), steps = min(8, (d - col + 31) >> 5);  // none past d
+        if (w > 0) {
+            const bf16 *src[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                src[nb] = nb * 8 + g < T ? a.x + (int64_t)(nb * 8 + g) * d : nullptr;
+            load_b<NB, false>(src, col, d, x);
+        }
+        const int mine = (steps - grp + (1 << gshift) - 1) >> gshift;  // steps of this warp
+#pragma unroll 1
+        for (int k0 = 0; k0 < mine; k0 += room) {
+            const int n = min(room, mine - k0);
+            const bf16 *wg = a.Wg + (int64_t)col * E, *wn = a.Wn + (int64_t)col * E;
+            __syncwarp();
+            if ((E & 7) == 0) {  // rows of whole 16-byte pieces
 #pragma unroll 4
-            for (int i = lane; i < n * 32 * NT; i += 32) {
-                const int k = i / NT, o = (i % NT) * 8;
-                const bf16 *src = o < E ? a.Wg + (k0 + k) * E + o : a.Wn + (k0 + k) * E + o - E;
-                cp16(sb + i * 16, src, true);
-            }
-            cp_commit();
-        }
-        // A: 8 consecutive columns of token rows g, g + 8
-        uint4 x0[8], x1[8];
-        const bf16 *xs = a.x + (int64_t)g * d + k0 + 8 * c;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            x0[s] = s < n && g < T ? ld_nc(xs + s * 32) : make_uint4(0, 0, 0, 0);
-            x1[s] = s < n && g + 8 < T ? ld_nc(xs + (int64_t)8 * d + s * 32) : make_uint4(0, 0, 0, 0);
-        }
-        if ((E & 7) != 0) {
-            const bf16 zero = __float2bfloat16_rn(0.f);
+                for (int i = lane; i < n * 32 * NT; i += 32) {
+                    const int k = NT == 1 ? i : i / NT, o = (i - k * NT) * 8;
+                    const int row = (grp + ((k0 + (k >> 5)) << gshift)) * 32 + (k & 31);
+                    cp16(sb + i * 16, o < E ? wg + (int64_t)row * E + o : wn + (int64_t)row * E + o - E, true);
+                }
+                cp_commit();
+                cp_wait<0>();
+            } else {
+                const bf16 zero = __float2bfloat16_rn(0.f);
 #pragma unroll 8
-            for (int i = lane; i < n * 32 * NP; i += 32) {
-                const int k = i / NP, o = i % NP;
-                reinterpret_cast<bf16 *>(stage)[i] =
-                    o < E ? a.Wg[(k0 + k) * E + o]
-                          : (o < nout ? a.Wn[(k0 + k) * E + o - E] : zero);
+                for (int i = lane; i < n * 32 * NP; i += 32) {
+                    const int k = i / NP, o = i - k * NP;
+                    const int row = (grp + ((k0 + (k >> 5)) << gshift)) * 32 + (k & 31);
+                    reinterpret_cast<bf16 *>(stage)[i] =
+                        o < E ? wg[(int64_t)row * E + o]
+                              : (o < nout ? wn[(int64_t)row * E + o - E] : zero);
+                }
             }
-        }
-        cp_wait<0>();
-        __syncwarp();
+            __syncwarp();
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            if (s >= n)
-                break;
-            // B of the two products: columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
-            const int i = lane & 7, kk = s * 32 + 8 * (i >> 1) + (i & 1) + 2 * (lane >> 3);
+            for (int b = 0; b < 8; ++b) {  // unrolled: x stays in registers
+                const int k = (b >> gshift) - k0;
+                if ((b & ((1 << gshift) - 1)) != grp || k < 0 || k >= n || b >= steps)
+                    continue;
+                // A: 8 consecutive columns of token rows g, g + 8.  B of the two products:
+                // columns 8c + {0,1 | 2,3} and 8c + {4,5 | 6,7}
+                const uint4 x0 = x[0][b], x1 = NB == 2 ? x[NB - 1][b] : make_uint4(0, 0, 0, 0);
+                const int i = lane & 7, kk = k * 32 + 8 * (i >> 1) + (i & 1) + 2 * (lane >> 3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint32_t b[4];
-                ldsm_x4_trans(sb + (uint32_t)(kk * NP * 2 + nt * 16), b);
-                mma_bf16_16816(acc[nt], x0[s].x, x1[s].x, x0[s].y, x1[s].y, b[0], b[1]);
-                mma_bf16_16816(acc[nt], x0[s].z, x1[s].z, x0[s].w, x1[s].w, b[2], b[3]);
+                for (int nt = 0; nt < 4; ++nt) {
+                    if (nt >= NT)
+                        break;
+                    uint32_t f[4];
+                    ldsm_x4_trans(sb + (uint32_t)(kk * NP * 2 + nt * 16), f);
+                    mma_bf16_16816(acc[nt], x0.x, x1.x, x0.y, x1.y, f[0], f[1]);
+                    mma_bf16_16816(acc[nt], x0.z, x1.z, x0.w, x1.w, f[2], f[3]);
+                }
             }
         }
     }
     float *pw = part + (size_t)warp * T * NP;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < 4; ++nt) {
         const int o = nt * 8 + 2 * c;
-        if (g < T) {
+        if (nt < NT && g < T) {
             pw[g * NP + o] = acc[nt][0];
             pw[g * NP + o + 1] = acc[nt][1];
         }
-        if (g + 8 < T) {
+        if (nt < NT && NB == 2 && g + 8 < T) {
             pw[(g + 8) * NP + o] = acc[nt][2];
             pw[(g + 8) * NP + o + 1] = acc[nt][3];
         }
@@ -646,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE];
     __shared__ int32_t s_idx[kMaxRows], s_slot[kMaxRows], s_rtok[kMaxRows];
     __shared__ int8_t s_map[kMaxE * MOE_MX4_FEW_TOKENS];  // row of (expert, token), -1 none
-    __shared__ float s_w[kMaxRows], s_rw[kMaxRows], s_inv[kMaxInv];
+    __shared__ float s_w[kMaxRows], s_rw[kMaxRows];
     __shared__ float s_lg[MOE_MX4_FEW_TOKENS * 32], s_prob[MOE_MX4_FEW_TOKENS * kMaxE],
         s_gw[MOE_MX4_FEW_TOKENS * kMaxE];
     __shared__ int32_t s_items[kItems];
@@ -657,12 +614,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     char *region = sm;  // the router's sums, GEMM 1's, then the rows of h
     char *my_ring = sm + kRegion + warp * 2 * kStageBytes;
     const uint32_t ring_s = smem_u32(my_ring);
-    // the grid barrier's generation before this launch's barrier (it changes only once
-    // every CTA has arrived, this one included)
-    int32_t gen = 0;
-    if (threadIdx.x == 0) {
+    // x first: this warp's slice of window 0, as it lies
+    UpPlan plan(d, NB);
+    const bf16 *xsrc[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+        xsrc[nb] = nb * 8 + g < T ? a.x + (int64_t)(nb * 8 + g) * d : nullptr;
+    uint4 xb[NB][8];
+    load_b<NB, false>(xsrc, plan.column(0), d, xb);
+    // The grid barrier counts arrivals for ever, gridDim.x a launch: this launch's are complete
+    // when the count reaches the next multiple.
+    unsigned long long target = 0;
+    if (threadIdx.x == kThreads - 1) {
         s_abort = 0;
-        gen = ld_acquire_gpu(a.gbar + 1);
+        const unsigned long long n = ld_acquire_u64(a.gbar);
+        target = (n / gridDim.x + 1) * gridDim.x;
     }
     s_map[threadIdx.x] = -1;
     if (threadIdx.x < kMaxE)
@@ -671,12 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
     float *part = reinterpret_cast<float *>(region);
-    switch ((nout + 7) / 8) {
-    case 1: router_logits<1>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
-    case 2: router_logits<2>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
-    case 3: router_logits<3>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
-    default: router_logits<4>(a, my_ring, 2 * kStageBytes, part, s_lg); break;
-    }
+    router_logits<NB>(a, plan, xb, my_ring, 2 * kStageBytes, part, s_lg);
     if (warp < T)
         gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
                         a.noise + (a.noise != nullptr ? (size_t)warp * E : 0), a.bias, a.router_type,
@@ -725,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         __syncwarp();
     }
     const int R = s_off[E], m8 = round_up(m, 8);
+    const Place place;
     uint32_t a_off[4];  // this lane's words of A row g in a chunk
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -734,12 +696,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     {
         const UpItems up(nsel, m);
         const int n_up = up.count();
-        UpPlan plan(d, NB);
         float *sums = reinterpret_cast<float *>(region);
         // sums of an item: [slice][half][nb][lane] float4
         const int nks = 1 << plan.kshift, ks = warp & (nks - 1);
-        uint4 xb[NB][8];
-        float inv[NB][2][2];
+        float inv[NB][2][2], one[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            one[nb] = 1.f;
 #pragma unroll 1
         for (int base = 0; base < n_up; base += kItems) {
             plan.n = min(kItems, n_up - base);
@@ -753,24 +716,26 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             __syncwarp();
             UpWalk ld(plan);
             if (ld.on(plan)) {
-                up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s);
+                up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s, place);
                 ld.next(plan);
             }
             uint32_t st = 0;
-            if (plan.n_win == 1)
-                load_slice<NB>(a, plan.column(0), xb, inv);
+            if (plan.n_win == 1 && base == 0)
+                scale_b<NB>(xb, plan.column(0), d, one, inv);
 #pragma unroll 1
             for (int b0 = 0; b0 < plan.n; b0 += plan.batch) {
                 const int b1 = min(b0 + plan.batch, plan.n);
 #pragma unroll 1
                 for (int w = 0; w < plan.n_win; ++w) {
-                    if (plan.n_win > 1)
-                        load_slice<NB>(a, plan.column(w), xb, inv);
+                    if (plan.n_win > 1) {
+                        load_b<NB, false>(xsrc, plan.column(w), d, xb);
+                        scale_b<NB>(xb, plan.column(w), d, one, inv);
+                    }
 #pragma unroll 1
                     for (int i = b0 + plan.group(); i < b1; i += plan.groups()) {
                         __syncwarp();  // the other stage has been read
                         if (ld.on(plan)) {
-                            up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s + (st ^ kStageBytes));
+                            up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s + (st ^ kStageBytes), place);
                             ld.next(plan);
                         } else {
                             cp_commit();
@@ -845,33 +810,30 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // ---- h of every CTA complete: a grid barrier; GEMM 2's first weights travel meanwhile,
     // and CTA 0 writes the routing, the tables and the statistics
     __syncthreads();  // h of this CTA is written
+    if (threadIdx.x == kThreads - 1)  // releases this CTA's h, ordered before by the barrier above
+        asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(a.gbar) : "memory");
+    const DownPlan down(a, nsel);
+    DownWalk ld(down);
+    if (ld.on(down)) {
+        down_fill(a, down, ld.strip, s_sel[ld.is], ld.u * kSlice, ring_s, place);
+        ld.next(down);
+    }
     if (threadIdx.x == kThreads - 1) {
-        __threadfence();  // this CTA's h, ordered before by the barrier above
-        if (atomicAdd(a.gbar, 1) == (int)gridDim.x - 1) {  // the last to arrive releases all
-            __threadfence();
-            asm volatile("red.relaxed.gpu.global.and.b32 [%0], 0;" ::"l"(a.gbar) : "memory");
-            __threadfence();
-            atomicAdd(a.gbar + 1, 1);
-        }
-    }
-    const DownPlan plan(a, nsel);
-    DownWalk ld(plan);
-    if (ld.on(plan)) {
-        down_fill(a, plan, ld.strip, s_sel[ld.is], ld.w * plan.win + ld.u * kSlice, ring_s);
-        ld.next(plan);
-    }
-    if (threadIdx.x == 0) {
-        const uint64_t t0 = globaltimer_ns();
-        while (ld_acquire_gpu(a.gbar + 1) == gen) {
-            if (globaltimer_ns() - t0 > a.wait_ns) {
+        uint64_t t0 = 0;
+        for (uint32_t i = 1; ld_acquire_u64(a.gbar) < target; ++i) {
+            if ((i & 15u) != 0)
+                continue;
+            const uint64_t now = globaltimer_ns();
+            t0 = t0 == 0 ? now : t0;
+            if (now - t0 > a.wait_ns) {
                 set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                 s_abort = 1;
                 break;
             }
         }
-    } else if (blockIdx.x == 0 && threadIdx.x >= 32) {
+    } else if (blockIdx.x == 0 && threadIdx.x < kThreads - 32) {
         constexpr int nt = kThreads - 32;
-        const int t1 = (int)threadIdx.x - 32;
+        const int t1 = (int)threadIdx.x;
         if (t1 < T * k) {
             a.idx[t1] = s_idx[t1];
             a.w[t1] = s_w[t1];
@@ -911,11 +873,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 
     // ---- GEMM 2 and the combine of this CTA's columns
     if (!s_abort) {
-        const int pitch = row_pitch(a.win2), strips = (4 * (plan.hi - plan.lo) + kStrip - 1) / kStrip;
-        const uint32_t region_s = smem_u32(region);
         uint32_t st = 0;
 #pragma unroll 1
-        for (int strip = 0; strip < strips; ++strip) {
+        for (int strip = 0; strip < down.strips; ++strip) {
             float acc[2][NB][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -924,81 +884,64 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         acc[h][nb][q] = 0.f;
+            int is = 0, u = warp;
 #pragma unroll 1
-            for (int w = 0; w < plan.n_win; ++w) {
-                const int units = plan.units(w), chunks = 2 * units;
-                if (strip + w > 0)
-                    __syncthreads();  // the region's last use is over
-                stage_rows(region, pitch, s_inv, R, w * a.win2, chunks, m, a.h, m8, s_rw);
-                __syncthreads();
-                int is = 0, u = warp;
-#pragma unroll 1
-                while (true) {
-                    while (u >= units) {
-                        u -= units;
-                        ++is;
-                    }
-                    if (is >= nsel)
-                        break;
-                    const int8_t *map = s_map + s_sel[is] * MOE_MX4_FEW_TOKENS;
-                    uint4 x[NB][8];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {  // a token elsewhere: a column of zeros
-                        const int row = map[nb * 8 + g];
-                        const uint32_t bp = region_s + (uint32_t)(row * pitch + u * kSlice * 2 + 16 * c);
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            x[nb][b] = make_uint4(0, 0, 0, 0);
-                            if (row >= 0)
-                                x[nb][b] = lds128(bp + b * 64);
-                        }
-                    }
-                    // 0 * sum would not do: a NaN weight stays with its tokens
-                    bool on[NB][2];
-                    float f[NB][2][2];
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int row = map[nb * 8 + 2 * c + j];
-                            on[nb][j] = row >= 0;
-                            const float *fi = s_inv + max(row, 0) * chunks + 2 * u;
-                            f[nb][j][0] = fi[0];
-                            f[nb][j][1] = fi[1];
-                        }
-                    __syncwarp();  // the other stage has been read
-                    if (ld.on(plan)) {
-                        down_fill(a, plan, ld.strip, s_sel[ld.is], ld.w * plan.win + ld.u * kSlice,
-                                  ring_s + (st ^ kStageBytes));
-                        ld.next(plan);
-                    } else {
-                        cp_commit();
-                    }
-                    cp_wait<1>();
-                    __syncwarp();
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float sum[NB][4];
-                            chunk_mma<NB>(sum, ring_s + st + (2 * h + v) * kChunkBytes, a_off,
-                                          [&](int nb, int b) { return x[nb][4 * v + b]; }, g);
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    if (on[nb][j]) {
-                                        acc[h][nb][j] = fmaf(sum[nb][j], f[nb][j][v], acc[h][nb][j]);
-                                        acc[h][nb][2 + j] =
-                                            fmaf(sum[nb][2 + j], f[nb][j][v], acc[h][nb][2 + j]);
-                                    }
-                        }
-                    st ^= kStageBytes;
-                    u += kWarps;
+            while (true) {
+                while (u >= down.units) {
+                    u -= down.units;
+                    ++is;
                 }
+                if (is >= nsel)
+                    break;
+                // column t of B: token t's row of this expert, zeros if it has none
+                const int8_t *map = s_map + s_sel[is] * MOE_MX4_FEW_TOKENS;
+                const bf16 *src[NB];
+                float w[NB], f[NB][2][2];
+                bool on[NB][2];
+                uint4 x[NB][8];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const int row = map[nb * 8 + g];
+                    src[nb] = row >= 0 ? a.h + (int64_t)row * m8 : nullptr;
+                    w[nb] = row >= 0 ? s_rw[row] : 0.f;
+                    // 0 * sum would not do: a NaN weight stays with its tokens
+                    on[nb][0] = map[nb * 8 + 2 * c] >= 0;
+                    on[nb][1] = map[nb * 8 + 2 * c + 1] >= 0;
+                }
+                load_b<NB, true>(src, u * kSlice, m, x);
+                __syncwarp();  // the other stage has been read
+                if (ld.on(down)) {
+                    down_fill(a, down, ld.strip, s_sel[ld.is], ld.u * kSlice, ring_s + (st ^ kStageBytes),
+                              place);
+                    ld.next(down);
+                } else {
+                    cp_commit();
+                }
+                scale_b<NB>(x, u * kSlice, m, w, f);
+                cp_wait<1>();
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float sum[NB][4];
+                        chunk_mma<NB>(sum, ring_s + st + (2 * h + v) * kChunkBytes, a_off,
+                                      [&](int nb, int b) { return x[nb][4 * v + b]; }, g);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (on[nb][j]) {
+                                    acc[h][nb][j] = fmaf(sum[nb][j], f[nb][v][j], acc[h][nb][j]);
+                                    acc[h][nb][2 + j] = fmaf(sum[nb][2 + j], f[nb][v][j], acc[h][nb][2 + j]);
+                                }
+                    }
+                st ^= kStageBytes;
+                u += kWarps;
             }
-            // the warps' sums over GEMM 2's finished rows of h: [warp][half][nb][lane] float4
-            __syncthreads();
+            if (strip > 0)
+                __syncthreads();  // the last strip's sums have been read
+            // the warps' sums: [warp][half][nb][lane] float4
             float4 *o = reinterpret_cast<float4 *>(region) + (size_t)warp * 2 * NB * 32 + lane;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -1013,8 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 // j: [half][nb][row bit 3][lane of the fragment][token bit 0]
                 const int L = j >> 1 & 31, hn = j >> 7, s = (hn / NB) * 16 + (j >> 6 & 1) * 8 + (L >> 2);
                 const int t = hn % NB * 8 + 2 * (L & 3) + (j & 1);
-                const int q = plan.lo + 8 * strip, col = down_column(q, s);
-                if (t < T && s < 4 * (plan.hi - q) && col < d) {
+                const int q = down.lo + 8 * strip, col = down_column(q, s);
+                if (t < T && s < 4 * (down.hi - q) && col < d) {
                     const float *r = sums + ((size_t)hn * 32 + L) * 4 + (j >> 6 & 1) * 2 + (j & 1);
                     float v = 0.f;
 #pragma unroll
@@ -1055,22 +998,7 @@ static cudaError_t grid_size(int *out)
     return cudaSuccess;
 }
 
-// Columns staged at once for R rows of h of K columns: all of them if they fit the region
-// and the table of scales, else as many whole slices as do.
-static int window(int rows, int K)
-{
-    const int all = (K + kSlice - 1) / kSlice * kSlice;
-    int w = (kRegion / rows - 64) / 2 / kSlice * kSlice;
-    const int t = kMaxInv / rows * kChunkCols / kSlice * kSlice;
-    w = w < t ? w : t;
-    return w < all ? w : all;
-}
-
 }  // namespace few
-
-static_assert(few::kRegion / few::kMaxRows >= 2 * few::kSlice + 64 &&
-                  few::kMaxInv / few::kMaxRows * few::kChunkCols >= few::kSlice,
-              "a slice of every row of h fits");
 
 bool mx4_few_fits(const moe_params_t *p, bool noisy)
 {
@@ -1110,7 +1038,7 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.kept = b->kept;
     a.offsets = b->offsets;
     a.status = reinterpret_cast<int32_t *>(ws);
-    a.gbar = a.status + kWsDecodeBarrierWord;
+    a.gbar = reinterpret_cast<unsigned long long *>(ws + kWsMx4BarrierWord * 4);
     a.wait_ns = wait_limit_ns();
     a.lambda = p->balance_lambda;
     a.scale = p->rescale ? (float)p->E / (float)p->k : 1.0f;
@@ -1121,7 +1049,6 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.k = p->k;
     a.C = p->capacity;
     a.router_type = p->router_type;
-    const int R = p->T * p->k;
     const int64_t r13 = 2 * round_up(p->m, 16);
     a.tk1 = (p->d + 127) / 128;
     a.tk2 = (p->m + 127) / 128;
@@ -1129,7 +1056,6 @@ cudaError_t launch_mx4_few(const moe_params_t *p, const moe_mx4_buffers_t *b, ch
     a.w13_scales = (r13 + 127) / 128 * a.tk1 * kMx4Tile;
     a.w2_codes = (int64_t)p->d * (mx4_k32(p->m) / 2);
     a.w2_scales = (int64_t)(p->d + 127) / 128 * a.tk2 * kMx4Tile;
-    a.win2 = window(R, p->m);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
