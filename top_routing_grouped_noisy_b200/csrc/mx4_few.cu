@@ -360,14 +360,17 @@ __device__ __forceinline__ void down_fill(const Args &a, const DownPlan &p, int 
 // 2^(13 - floor(log2(max))), exponent field 127 + 13 - (E - 127), at most 254.
 __device__ __forceinline__ uint32_t scale_field(uint32_t top) { return min(267u - (top >> 7), 254u); }
 
+// largest magnitude bits of two bf16 values in each half of a word: max of the halves, apart
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t top_of(const uint4 &v)
 {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
-    return top;
+    return max_halves(max_halves(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                      max_halves(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
 }
 
 // 8 bf16 values times mul, as f16
@@ -433,10 +436,10 @@ __device__ __forceinline__ void scale_b(uint4 (&xb)[NB][8], int col, int limit, 
             uint32_t top = 0;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                top = max(top, top_of(xb[nb][4 * u + b]));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t field = scale_field(top);
+                top = max_halves(top, top_of(xb[nb][4 * u + b]));
+            top = max_halves(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max_halves(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t field = scale_field(max(top & 0xffffu, top >> 16));
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 to_half(xb[nb][4 * u + b], __uint_as_float(field << 23));
