@@ -197,7 +197,7 @@ cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
                           void *hs, int32_t *status, cudaStream_t s);
 cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *hs,
                             const int32_t *offsets, const void *W2q, const void *W2s, void *out,
-                            int32_t *status, cudaStream_t s);
+                            bool after_up, int32_t *status, cudaStream_t s);
 
 // the whole layer for 1..16 tokens on mx4 weights and bf16 activations (cooperative)
 bool mx4_few_fits(const moe_params_t *p, bool noisy);

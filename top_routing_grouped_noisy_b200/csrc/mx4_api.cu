@@ -216,7 +216,7 @@ int moe_expert_down_mx4(const moe_params_t *p, const void *h_q, const void *h_s,
     MX_TOK(out);
     if (p->T == 0)
         return report_ok();
-    return mx_after(fn, launch_mx4_down(p, h_q, h_s, offsets, W2_q, W2_s, out,
+    return mx_after(fn, launch_mx4_down(p, h_q, h_s, offsets, W2_q, W2_s, out, false,
                                         reinterpret_cast<int32_t *>(ws), (cudaStream_t)stream));
 }
 
@@ -233,9 +233,10 @@ int moe_expert_ffn_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
     MX_PTR(W2_s);
     MX_TOK(out);
     if ((rc = moe_expert_up_mx4(p, x_q, x_s, offsets, W13_q, W13_s, h_q, h_s, ws, ws_bytes,
-                                stream)) != MOE_OK)
+                                stream)) != MOE_OK || p->T == 0)
         return rc;
-    return moe_expert_down_mx4(p, h_q, h_s, offsets, W2_q, W2_s, out, ws, ws_bytes, stream);
+    return mx_after(fn, launch_mx4_down(p, h_q, h_s, offsets, W2_q, W2_s, out, true,
+                                        reinterpret_cast<int32_t *>(ws), (cudaStream_t)stream));
 }
 
 int moe_forward_mx4(const moe_params_t *p, const moe_mx4_buffers_t *b, int32_t act, void *ws,
@@ -301,8 +302,8 @@ int moe_forward_mx4(const moe_params_t *p, const moe_mx4_buffers_t *b, int32_t a
                                      s)) == cudaSuccess &&
             (e = launch_mx4_up(p, b->x_q, b->x_s, b->offsets, b->W13_q, b->W13_s, b->h_q, b->h_s,
                                status, s)) == cudaSuccess &&
-            (e = launch_mx4_down(p, b->h_q, b->h_s, b->offsets, b->W2_q, b->W2_s, b->out, status,
-                                 s)) == cudaSuccess)
+            (e = launch_mx4_down(p, b->h_q, b->h_s, b->offsets, b->W2_q, b->W2_s, b->out, true,
+                                 status, s)) == cudaSuccess)
             e = launch_combine(p, b->out, b->slot_row, b->topk_w, b->y, s);
     }
     if (e == cudaSuccess)
