@@ -4,8 +4,11 @@
 // Mixtral and ST types); capacity: its "容量因子"; SwiGLU expert: "LLaMA-MoE v2", code
 // sample, class Expert; statistics: "LLaMA-MoE v2", section "门控机制设计".
 //
-// Bound by the selected experts' weights (0.53 bytes each), then by the chain
-// routing -> GEMM 1 -> grid barrier -> GEMM 2.
+// The selected experts' weights (0.53 bytes each) are all it has to read; the integer pipe (the
+// conversions of their codes) and the chain routing -> GEMM 1 -> grid barrier -> GEMM 2 take
+// longer.  Measured (d 4096, graph replays): 1 token of 8 experts x 1376, top 2, 18.5 us (18.2 MB,
+// 0.98 TB/s), 8 tokens 33.5 us (65 MB, 1.9 TB/s), 16 tokens of 16 x 688, top 4, 55.7 us (71 MB,
+// 1.3 TB/s).
 //
 //   routing   every CTA computes all logits (mma.sync on bf16), gates and tables: x and W_g
 //             are some ten KB and no CTA waits for another.

@@ -16,10 +16,15 @@
 //
 // Work: tiles of 128 rows x BN columns over every expert, listed on the device from the
 // offsets.  A tile's A rows come in boxes of 32, as many as it has: a TMA box costs the copy
-// engine about 3.5 cycles a 128-byte row whether the row exists or not, and with few rows that
-// bounds the kernel (T = 1: 128-row boxes took 0.38 us a stage).  TMEM: two accumulators of BN columns, then the scale columns (24 per set,
-// four sets).  Roles as in the bf16 kernel: warp 0 TMA producer, warp 1 TMEM allocator
-// and issuer, warps 2-9 epilogue (each thread one row, half of the columns).
+// engine 2 to 4 cycles a 128-byte row whether the row exists or not (4 where rows do not start
+// on 128-byte lines), and with few rows that bounds the kernel (1 token, 128-row boxes: 0.38 us
+// a stage, a third of it W's rows).  TMEM: two accumulators of BN columns, then a set of 24 scale
+// columns for each stage.  Roles: warp 0 TMA producer, warp 1 TMEM allocator and issuer, warps
+// 2-9 epilogue (each thread one row, half of the columns).
+//
+// Measured (d 4096, m 1376, 8 experts, top 2; a3 / a4): 1 token 7.9 / 5.9 us (weights 11.9 and
+// 6.0 MB), 203 tokens 13.8 / 9.3, 16384 tokens 133 / 105 (5.57 and 3.52 PFLOP/s, the pair
+// kernels).
 //
 // Every mbarrier wait is bounded: past the limit the kernel records
 // MOE_ERR_DEVICE_TIMEOUT, stops every role, drains its copies and products (bounded
@@ -86,7 +91,7 @@ struct Geo {
 
 // The producer and the issuer run their loops as whole warps and let one elected lane issue:
 // the loops' values stay in uniform registers, where copies and products take their operands
-// (a loop of one lane spends about 450 cycles a stage on moving them, as long as the
+// (a loop of one lane spent about 450 cycles a stage on moving them, as long as the
 // products take).  The warp number is made uniform the same way.
 __device__ __forceinline__ bool elect_one()
 {
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int nbt = min(G::BT, trb - nb0);  // B scale tiles that exist
             const uint8_t *sb_src = a.b_s + ((int64_t)t.e * trb + nb0) * tk * kMx4Tile;
             for (int kb = kb0; kb < num_kb; ++kb) {
-                if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const Tile t = decode_tile<BN>(aux, tile);
             // first B scale column inside the copied tiles: one column per 32 rows
             const uint32_t b_shift = (uint32_t)(t.n0 % 128 / 32);
-            if (!mbar_wait_spin(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
+            if (!mbar_wait(smem_u32(&aux->tempty[acc]), acc_phase ^ 1u, a.wait_ns, abort_flag,
                            a.status)) {
                 ok = false;
                 break;
@@ -426,7 +431,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag, a.status)) {
+                if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = decode_tile<BN>(aux, tile);
-            if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
+            if (!mbar_wait(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
                 break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
@@ -539,9 +544,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // ------------------------------------------------------------------------ 2-SM variant
 // cta_group::2: a cluster of two CTAs owns a 256 x 256 tile.  CTA r loads rows [128r, 128r +
 // 128) of A and of B with A's scales for its rows and B's for all 256 (every CTA's
-// accumulators see all columns); the leader issues M = 256 products.  The 1-SM kernel is bound
-// by the bytes that L2 hands to the SMs (43 KB per 128 x 192 x 256, about 30 bytes a cycle and
-// SM); here 35 KB serve 128 x 256 x 256 of each SM's work.
+// accumulators see all columns); the leader issues M = 256 products.  The 1-SM kernel copies 320
+// rows for 128 x 192 x 256 of work; here 256 rows serve 128 x 256 x 256 of each SM's.
+// A product of 256 x 256 x 64 takes 118 cycles; 5.57 PFLOP/s at 16384 tokens are 84% of four
+// times the measured bf16 rate.
 //
 // TMEM.  Two 256-column accumulators do not leave room for scales, so they share 64 columns:
 // accumulator 0 is columns 0..255, accumulator 1 columns 192..447, scales 448..471 and 480..503
@@ -671,18 +677,6 @@ __device__ __forceinline__ void commit_own(uint32_t bar)
                  : "memory");
 }
 
-// Epilogue warps w and w + 4 read the same TMEM lanes, one at a time: the warp without shared
-// columns lets the other's first load pass (taken in any order, the next tile's products start
-// about 900 cycles later).  Named barriers 1..4, one for each quarter of the lanes.
-__device__ __forceinline__ void pair_go(int warp)
-{
-    asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-}
-__device__ __forceinline__ void pair_wait(int warp)
-{
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-}
-
 // Tile order inside an expert: bands of `band` row tiles, row tiles fastest inside a band,
 // then the band's column tiles (as in the bf16 pair kernel).
 __device__ __forceinline__ Tile decode(const Aux *aux, int tile, int n_tiles, int band)
@@ -788,7 +782,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int sa_row = (int)mx4_expert_tile(t.off, t.e) + (t.row0 - t.off) / BM + (int)rank;
             const int sb_row = t.e * trb + t.n0 / 128;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -831,7 +825,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t lo0 = desc_lo(smem_base);
             for (int tile = cluster_id; tile < total && ok; tile += nclusters, ++ti) {
                 // the shared columns of the tile before have been read
-                if (ti > 0 && !mbar_wait_spin(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
                                          abort_flag, a.status)) {
                     ok = false;
                     break;
@@ -841,9 +835,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int kb = 0; kb < num_kb; ++kb) {
                     // the products of two stages ago are done with this set of scales (before
                     // the third stage there are none)
-                    if (!mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                    if (!mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
                                    a.status) ||
-                        (!first && !mbar_wait_spin(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                        (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
                                               abort_flag, a.status))) {
                         ok = false;
                         break;
@@ -900,7 +894,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int tile = cluster_id; tile < total; tile += nclusters, ++ti) {
             const Tile t = decode(aux, tile, n_tiles, band);
             const int acc = ti & 1;
-            if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+            if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                            a.status))
                 break;
             tc_fence_after();
@@ -916,8 +910,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
                 uint32_t v[2][32];
-                if (!shares && i == 0)
-                    pair_wait(warp);
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                 tmem_wait_ld();
@@ -926,7 +918,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_cluster(tfree0);
-                    pair_go(warp);
                 }
                 if constexpr (EPI == EPI_UP) {
                     const int nb = t.n0 / 2 + gi * 32;  // 32 neurons: one block of h
@@ -968,10 +959,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // ------------------------------------------------------------------------ resident A
 // The second product has few stages along K (at most kResKb) and, per stage, 256 rows to load
-// for 256 x 256 x 256 of work, which is what bounds it (about 3.3 cycles a 128-byte row and
-// SM).  Here a pair keeps the A rows of its tile, all of K, in shared memory while it walks
-// over a chunk of column tiles, so only B is loaded per stage.  A's K blocks are freed one by
-// one by the chunk's last tile (aempty) and refilled for the next one behind it.
+// for 256 x 256 x 256 of work; with m = 1376 they do not start on 128-byte lines and take about
+// twice the copy engine's time of those that do.  Here a pair keeps the A rows of its tile, all
+// of K, in shared memory while it walks over a chunk of column tiles, so only B is loaded per
+// stage.  A's K blocks are freed one by one by the chunk's last tile (aempty) and refilled for the next one behind it.  Measured, with
+// the kernel above / this one: 16384 tokens (d 4096, m 1376, top 2) 119.5 / 106 us, 4096 tokens
+// (16 experts, m 688, top 4) 40.4 / 38 us.
 //   afull[kb]  leader: both CTAs' bytes      aempty[kb]  both CTAs: the leader's commit
 constexpr int kResKb = 6;
 constexpr int RES_STAGE = B_BYTES + SFB;   // 18 KB
@@ -1129,7 +1122,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int b_row = nt * BN + (int)rank * BNH, sb_row = u.e * trb + nt * (BN / 128);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (nt == u.n_lo) {
-                        if (!mbar_wait_spin(smem_u32(&aux->aempty[kb]), (uint32_t)(nu & 1) ^ 1u, a.wait_ns,
+                        if (!mbar_wait(smem_u32(&aux->aempty[kb]), (uint32_t)(nu & 1) ^ 1u, a.wait_ns,
                                        abort_flag, a.status)) {
                             ok = false;
                             break;
@@ -1143,7 +1136,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                         ++a_fills;
                     }
-                    if (!mbar_wait_spin(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
+                    if (!mbar_wait(smem_u32(&aux->empty[stage]), phase ^ 1u, a.wait_ns, abort_flag,
                                    a.status)) {
                         ok = false;
                         break;
@@ -1192,7 +1185,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const ResUnit u = res_unit(aux, unit, n_tiles, nchunks);
                 for (int nt = u.n_lo; nt < u.n_hi && ok; ++nt, ++ti) {
                     // the shared columns of the tile before have been read
-                    if (ti > 0 && !mbar_wait_spin(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
+                    if (ti > 0 && !mbar_wait(smem_u32(&aux->tfree), (uint32_t)(ti - 1) & 1u, a.wait_ns,
                                              abort_flag, a.status)) {
                         ok = false;
                         break;
@@ -1201,11 +1194,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t d_tmem = tmem_base + (uint32_t)((ti & 1) * ACC_STEP);
                     for (int kb = 0; kb < num_kb; ++kb) {
                         // with the products of two stages ago done this set of scales is free
-                        if ((nt == u.n_lo && !mbar_wait_spin(smem_u32(&aux->afull[kb]), (uint32_t)nu & 1u,
+                        if ((nt == u.n_lo && !mbar_wait(smem_u32(&aux->afull[kb]), (uint32_t)nu & 1u,
                                                         a.wait_ns, abort_flag, a.status)) ||
-                            !mbar_wait_spin(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
+                            !mbar_wait(smem_u32(&aux->full[stage]), phase, a.wait_ns, abort_flag,
                                        a.status) ||
-                            (!first && !mbar_wait_spin(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
+                            (!first && !mbar_wait(smem_u32(&aux->empty[old]), old_phase, a.wait_ns,
                                                   abort_flag, a.status))) {
                             ok = false;
                             break;
@@ -1269,7 +1262,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int row0 = u.row0 + (int)rank * BM + lane_base, row = row0 + lane;
             for (int nt = u.n_lo; nt < u.n_hi; ++nt, ++ti) {
                 const int acc = ti & 1;
-                if (!mbar_wait_spin(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+                if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -1284,8 +1277,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int i = 0; i < 2; ++i) {
                     const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
                     uint32_t v[2][32];
-                    if (!shares && i == 0)
-                        pair_wait(warp);
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                     tmem_wait_ld();
@@ -1294,7 +1285,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive_cluster(tfree0);
-                        pair_go(warp);
                     }
                     store_64(a, v, nt * BN + gi * 64, row0, row, u.row_end, st);
                     __syncwarp();  // the next tcgen05.ld takes the whole warp
@@ -1417,9 +1407,45 @@ static cudaError_t scale_map(CUtensorMap *map, const void *base, uint64_t tk, ui
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows (T*k) from which the 2-SM kernel is used; below it the 1-SM kernel spreads the few
-// tiles over more SMs.
-constexpr int64_t kPairMinRows = 4096;
+// Which kernel and tile width.  The 1-SM kernel is bound by the 128-byte rows that a stage
+// copies, so its cost is waves (tiles over the SMs) x those rows: A's of an average tile in
+// boxes of 32, and B's.  A wave of the pair kernels and their longer start cost as much as the
+// rows below, fitted to times at 1 to 64 experts, 2 to 12000 rows and 1 to 16 stages.  Row
+// tiles are estimated for T*k rows spread evenly over the experts; each ragged end adds half a
+// tile.  Measured (d 4096, m 1376, us; 192 / 128 / 64 / pair):
+//   UP,   8 experts:  16 rows 11 / 13 / 17 / 18; 1024 rows 18 / 16 / 25 / 19;
+//                     2048 rows 21 / 22 / 36 / 20; 8192 rows 53 / 65 / 108 / 42
+//   UP,   1 expert:   200 rows 10 / 8.9 / 8.4 / 11; 1536 rows 17 / 16 / 25 / 12
+//   DOWN, 8 experts:  406 rows 10 / 8.6 / 11 / 12; 2048 rows 17 / 20 / 25 / 18;
+//                     8192 rows 49 / 52 / 74 / 33
+struct Choice {
+    bool two;
+    int bn;
+};
+static Choice choose(const DevInfo &di, int64_t rows, int E, int N, int num_kb, bool resident)
+{
+    const int64_t hit = rows < E ? rows : E;
+    auto row_tiles = [&](int bm) {
+        const int64_t t = (2 * rows + (int64_t)bm * (hit - 1) + 2 * bm - 1) / (2 * bm);
+        return t > hit ? t : hit;
+    };
+    const int64_t avg = (rows + hit - 1) / hit;
+    const int a_rows = avg >= BM ? BM : ((int)avg + kABox - 1) / kABox * kABox;
+    const int64_t pairs = row_tiles(2 * BM) * ((N + pair::BN - 1) / pair::BN);
+    Choice c = {true, 0};
+    const int start = resident ? 23000 / (15 * num_kb + 38) : 2400 / num_kb;
+    const int wave = resident ? 250 + 170 / num_kb : 280;
+    int64_t best = (pairs + di.pair_clusters - 1) / di.pair_clusters * wave + start;
+    for (int w : {192, 128, 64}) {
+        const int64_t tiles = row_tiles(BM) * ((N + w - 1) / w);
+        const int64_t cost = (tiles + di.sms - 1) / di.sms * (a_rows + w);
+        if (cost < best) {
+            best = cost;
+            c = {false, w};
+        }
+    }
+    return c;
+}
 
 template <int EPI, int BN>
 static cudaError_t launch_1sm(const DevInfo &di, const CUtensorMap &ta, const CUtensorMap &tb,
@@ -1437,22 +1463,11 @@ static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const
     cudaError_t e = prepare_device(&di);
     if (e != cudaSuccess)
         return e;
-    const bool two = rows >= kPairMinRows;
-    // 1-SM tile width: the fewest columns on the busiest SM when every reached expert has one
-    // row tile, the wider of equal ones
-    int bn = 192;
-    if (!two) {
-        const int64_t hit = rows < args.E ? rows : args.E;
-        int64_t best = INT64_MAX;
-        for (int w : {192, 128, 64}) {
-            const int64_t tiles = hit * ((args.N + w - 1) / w);
-            const int64_t cost = (tiles + di->sms - 1) / di->sms * w;
-            if (cost < best) {
-                best = cost;
-                bn = w;
-            }
-        }
-    }
+    const int num_kb = (args.K32 + BKC - 1) / BKC;
+    const bool resident = EPI == EPI_DOWN && num_kb <= pair::kResKb;
+    const Choice ch = choose(*di, rows, args.E, args.N, num_kb, resident);
+    const bool two = ch.two;
+    const int bn = ch.bn;
     // code rows as 2-byte elements (four codes each): the maps only copy
     const uint64_t kel = (uint64_t)args.K32 / 4, pitch = (uint64_t)args.K32 / 2;
     CUtensorMap ta, tb, to = {};
@@ -1483,8 +1498,7 @@ static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const
         return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    const int num_kb = (args.K32 + BKC - 1) / BKC;
-    if (EPI == EPI_DOWN && num_kb <= pair::kResKb) {
+    if (resident) {
         cluster_config(&cfg, attr, di->pair_clusters, pair::res_smem(num_kb), s);
         return cudaLaunchKernelEx(&cfg, pair::mx4_down_res_kernel, ta, tb, tsa, tsb, to, args,
                                   pair::res_stages(num_kb));

@@ -85,30 +85,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
-// The same wait for handshakes on the critical path: reading %globaltimer takes about 1500
-// cycles, so the clock and the abort flag are looked at once in 64 tries only.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                               volatile int32_t *abort_flag, int32_t *status)
-{
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try(bar, parity))
-            return true;
-        if ((i & 63u) != 0)
-            continue;
-        if (*abort_flag)
-            return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0)
-            t0 = now;
-        if (now - t0 > limit_ns) {
-            set_status(status, MOE_ERR_DEVICE_TIMEOUT);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
-
 // Bounded wait used while draining on exit (ignores the abort flag).
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
