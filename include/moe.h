@@ -465,8 +465,9 @@ int moe_mx4_dequantize(const void *codes, const void *scales, int32_t dtype, int
 
 /* a2's row copy in mx4: quantises every token row of x [T][d] (dtype of p) once and
  * writes it to each row its kept assignments own: x_q, x_s in the layout above.
- * topk_idx, slot_row and offsets are moe_dispatch_rows' outputs (a slot of -1, or an
- * expert outside [0,E), is skipped). */
+ * topk_idx, slot_row and offsets are moe_dispatch_rows' outputs (a slot of -1 or not
+ * below T*k, an expert outside [0,E), and a slot before its expert's offset are
+ * skipped). */
 int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_idx,
                      const int32_t *slot_row, const int32_t *offsets, void *x_q, void *x_s,
                      void *stream);
@@ -474,7 +475,9 @@ int moe_mx4_dispatch(const moe_params_t *p, const void *x, const int32_t *topk_i
 /* a3 on mx4 operands: h = silu(xq W1_e^T) * (xq W3_e^T) for the kept rows, where xq are
  * the values of x_q / x_s, accumulated in f32 by block-scaled tcgen05 products; h is
  * quantised from f32 into h_q / h_s (blocks of 32 neurons; neurons >= m are zeros).
- * Rows past offsets[E] are left as they were. */
+ * Rows past offsets[E] are left as they were.  Offsets that moe_dispatch_rows cannot
+ * have written (negative, falling, above T*k) set MOE_ERR_DEVICE_BADINDEX in ws and
+ * are taken as the nearest that can be; so in moe_expert_down_mx4. */
 int moe_expert_up_mx4(const moe_params_t *p, const void *x_q, const void *x_s,
                       const int32_t *offsets, const void *W13_q, const void *W13_s, void *h_q,
                       void *h_s, void *ws, size_t ws_bytes, void *stream);

@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     if (threadIdx.x == kThreads - 1) {
         uint64_t t0 = 0;
         for (uint32_t i = 1; ld_acquire_u64(a.gbar) < target; ++i) {
-            if ((i & 15u) != 0)
+            if ((i & 3u) != 0)
                 continue;
             const uint64_t now = globaltimer_ns();
             t0 = t0 == 0 ? now : t0;

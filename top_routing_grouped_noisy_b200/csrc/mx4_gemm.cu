@@ -105,6 +105,15 @@ __device__ __forceinline__ int warp_number()
     return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 }
 
+// A wait of a whole warp, with one answer: the lanes' clocks may differ at the limit, and the
+// epilogue's tcgen05.ld takes all lanes.  (The producer's and the issuer's waits are followed by
+// nothing that does.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile int32_t *abort_flag, int32_t *status)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, abort_flag, status));
+}
+
 // Descriptors, low and high words (bit 16 of the low word: the leading byte offset, unused by
 // the swizzled tiles and absent from the scale tiles').  Operand tiles: K-major, 128-byte swizzle (as tc::sdesc);
 // scale tiles: 32 rows of 16 bytes, no swizzle, 8-row groups 128 bytes apart.
@@ -162,12 +171,51 @@ struct GemmArgs {
     void *out;                 // DOWN: bf16 [rows][ld]; UP: h codes [rows][h32/2]
     uint8_t *h_s;              // UP: scales of h
     int E, N, K32;             // N: rows of an expert's matrix
+    int32_t rows;              // T*k
     int n_valid;               // UP: neurons m; DOWN: columns d
     int ld;                    // DOWN: d; UP: h32 / 2
     int after_up;              // DOWN: the kernel before in the stream is this call's UP
     int32_t *status;
     uint64_t wait_ns;
 };
+
+// The offsets and, times `per`, the number of row tiles (ROWS high) before each expert, by one
+// warp.  Offsets that no dispatch writes (below 0, above T*k, falling) are reported and taken as
+// the nearest that keep every row inside the buffers.
+template <int ROWS>
+__device__ __forceinline__ void load_offsets(const GemmArgs &a, int32_t *off, int32_t *start, int per)
+{
+    const int lane = threadIdx.x & 31;
+    int32_t top = 0, tiles = 0;  // offset and row tiles up to the 32 experts before
+    for (int i0 = 0; i0 <= a.E; i0 += 32) {
+        const bool in = i0 + lane <= a.E;
+        const int32_t given = in ? a.offsets[i0 + lane] : 0;
+        int32_t v = max(top, min(given, a.rows));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            v = lane >= o ? max(v, u) : v;
+        }
+        int32_t before = __shfl_up_sync(0xffffffffu, v, 1);
+        before = lane == 0 ? (i0 == 0 ? v : top) : before;
+        int32_t t = (v - before + ROWS - 1) / ROWS;  // of expert i0 + lane - 1
+        t += lane == 0 ? tiles : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, t, o);
+            t += lane >= o ? u : 0;
+        }
+        if (in) {
+            if (v != given)
+                set_status(a.status, MOE_ERR_DEVICE_BADINDEX);
+            off[i0 + lane] = v;
+            start[i0 + lane] = t * per;
+        }
+        top = __shfl_sync(0xffffffffu, v, 31);
+        tiles = __shfl_sync(0xffffffffu, t, 31);
+    }
+    __syncwarp();
+}
 
 // 32 accumulator columns c..c+31 of this thread's row: 16 gate and 16 up values
 __device__ __forceinline__ void swiglu16(const uint32_t (&v)[32], float *h)
@@ -296,17 +344,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     const int n_tiles = (a.N + BN - 1) / BN;
     if (warp == 2) {
-        for (int i = lane; i <= a.E; i += 32)
-            aux->off[i] = a.offsets[i];
-        __syncwarp();
-        if (lane == 0) {
-            int acc = 0;
-            for (int e = 0; e < a.E; ++e) {
-                aux->tstart[e] = acc;
-                acc += (aux->off[e + 1] - aux->off[e] + BM - 1) / BM * n_tiles;
-            }
-            aux->tstart[a.E] = acc;
-        }
+        load_offsets<BM>(a, aux->off, aux->tstart, n_tiles);
     }
     tc_fence_before();
     __syncthreads();
@@ -492,7 +530,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t acc_phase = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = decode_tile<BN>(aux, tile);
-            if (!mbar_wait(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
+            if (!warp_wait(smem_u32(&aux->tfull[acc]), acc_phase, a.wait_ns, abort_flag, a.status))
                 break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * BN);
@@ -531,6 +569,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0)
             bulk_wait_all();  // this lane's output stores are done before the CTA exits
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -740,17 +779,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     const int n_tiles = (a.N + BN - 1) / BN;
     if (warp == 2) {
-        for (int i = lane; i <= a.E; i += 32)
-            aux->off[i] = a.offsets[i];
-        __syncwarp();
-        if (lane == 0) {
-            int acc = 0;
-            for (int e = 0; e < a.E; ++e) {
-                aux->tstart[e] = acc;
-                acc += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM) * n_tiles;
-            }
-            aux->tstart[a.E] = acc;
-        }
+        load_offsets<2 * BM>(a, aux->off, aux->tstart, n_tiles);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -894,7 +923,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int tile = cluster_id; tile < total; tile += nclusters, ++ti) {
             const Tile t = decode(aux, tile, n_tiles, band);
             const int acc = ti & 1;
-            if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+            if (!warp_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                            a.status))
                 break;
             tc_fence_after();
@@ -936,6 +965,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0)
             bulk_wait_all();  // this lane's output stores are done before the CTA exits
     }
+    __syncwarp();
     tc_fence_before();
     cluster_sync();
     // after an abort, give copies still in flight time to land before either CTA of
@@ -1059,34 +1089,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     const int n_tiles = (a.N + BN - 1) / BN;
     if (warp == 2) {
+        load_offsets<2 * BM>(a, aux->off, aux->ustart, 1);
+        // column tiles per chunk, 1 << lane: the fewest loads on the busiest pair, A counting as
+        // much as one column tile's B; the smaller of equal ones
+        const int mt = aux->ustart[a.E], c = 1 << min(lane, 4);
+        const int64_t units = (int64_t)mt * ((n_tiles + c - 1) / c);
+        int64_t best = ((units + nclusters - 1) / nclusters * (min(c, n_tiles) + 1) << 5) + c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const int chunk = (int)(best & 31), nchunks = (n_tiles + chunk - 1) / chunk;
         for (int i = lane; i <= a.E; i += 32)
-            aux->off[i] = a.offsets[i];
-        __syncwarp();
-        if (lane == 0) {
-            int mt = 0;
-            for (int e = 0; e < a.E; ++e)
-                mt += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM);
-            // column tiles per chunk: the fewest loads on the busiest pair, A counting as much
-            // as one column tile's B
-            int best = 1;
-            int64_t best_cost = INT64_MAX;
-            for (int c = 1; c <= 16; c *= 2) {
-                const int64_t units = (int64_t)mt * ((n_tiles + c - 1) / c);
-                const int64_t cost = (units + nclusters - 1) / nclusters * (min(c, n_tiles) + 1);
-                if (cost < best_cost) {
-                    best_cost = cost;
-                    best = c;
-                }
-            }
-            aux->chunk = best;
-            const int nchunks = (n_tiles + best - 1) / best;
-            int acc = 0;
-            for (int e = 0; e < a.E; ++e) {
-                aux->ustart[e] = acc;
-                acc += (aux->off[e + 1] - aux->off[e] + 2 * BM - 1) / (2 * BM) * nchunks;
-            }
-            aux->ustart[a.E] = acc;
-        }
+            aux->ustart[i] *= nchunks;
+        if (lane == 0)
+            aux->chunk = chunk;
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -1262,7 +1278,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int row0 = u.row0 + (int)rank * BM + lane_base, row = row0 + lane;
             for (int nt = u.n_lo; nt < u.n_hi; ++nt, ++ti) {
                 const int acc = ti & 1;
-                if (!mbar_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
+                if (!warp_wait(smem_u32(&aux->tfull[acc]), (uint32_t)(ti >> 1) & 1u, a.wait_ns, abort_flag,
                                a.status)) {
                     ok = false;
                     break;
@@ -1294,6 +1310,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0)
             bulk_wait_all();  // this lane's output stores are done before the CTA exits
     }
+    __syncwarp();
     tc_fence_before();
     cluster_sync();
     if (threadIdx.x == 0) {  // after an abort, as in the kernel above
@@ -1456,9 +1473,9 @@ static cudaError_t launch_1sm(const DevInfo &di, const CUtensorMap &ta, const CU
 }
 
 template <int EPI>
-static cudaError_t launch_gemm(const void *A, int64_t rows, const void *B, const GemmArgs &args,
-                               cudaStream_t s)
+static cudaError_t launch_gemm(const void *A, const void *B, const GemmArgs &args, cudaStream_t s)
 {
+    const int64_t rows = args.rows;
     DevInfo *di = nullptr;
     cudaError_t e = prepare_device(&di);
     if (e != cudaSuccess)
@@ -1522,6 +1539,7 @@ cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
     a.out = hq;
     a.h_s = (uint8_t *)hs;
     a.E = p->E;
+    a.rows = p->T * p->k;
     a.N = 2 * round_up(p->m, 16);
     a.K32 = p->d;
     a.n_valid = p->m;
@@ -1529,7 +1547,7 @@ cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
     a.status = status;
     a.wait_ns = wait_limit_ns();
     count_launch();
-    return mxg::launch_gemm<mxg::EPI_UP>(xq, (int64_t)p->T * p->k, W13q, a, s);
+    return mxg::launch_gemm<mxg::EPI_UP>(xq, W13q, a, s);
 }
 
 cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *hs,
@@ -1542,6 +1560,7 @@ cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *h
     a.offsets = offsets;
     a.out = out;
     a.E = p->E;
+    a.rows = p->T * p->k;
     a.N = p->d;
     a.K32 = mx4_k32(p->m);
     a.n_valid = p->d;
@@ -1550,7 +1569,7 @@ cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *h
     a.status = status;
     a.wait_ns = wait_limit_ns();
     count_launch();
-    return mxg::launch_gemm<mxg::EPI_DOWN>(hq, (int64_t)p->T * p->k, W2q, a, s);
+    return mxg::launch_gemm<mxg::EPI_DOWN>(hq, W2q, a, s);
 }
 
 }  // namespace moe

@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kThreads)
             if (row < 0 || e < 0 || e >= E)
                 continue;
             const int off = offsets[e];
+            if (row >= Tn * k || off < 0 || off > row)
+                continue;  // no dispatch writes such tables; the buffers end here
             if (b * 32 < d)
                 st_v4(xq + (int64_t)row * (d / 2) + b * 16, c);
             xs[mx4_scale_at(mx4_expert_tile(off, e), tk, row - off, b)] = (uint8_t)byte;
