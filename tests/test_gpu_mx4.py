@@ -258,7 +258,7 @@ EXPERT_CASES = [  # T, E, k, m, d, capacity
     (64, 4, 2, 172, 512, -1), (129, 1, 1, 96, 256, -1), (200, 8, 2, 344, 288, -1),
     (300, 5, 2, 130, 224, 50), (700, 3, 2, 200, 1024, -1), (40, 64, 8, 48, 128, -1),
     (256, 2, 1, 1376, 320, -1),
-    # 4096 rows and more: CTA pairs, one or several column tiles, ragged ends
+    # thousands of rows: wider tiles, one or several of them, ragged ends
     (4096, 1, 1, 64, 96, -1), (2100, 3, 2, 200, 320, -1), (1500, 8, 3, 136, 544, 450),
     (2300, 5, 2, 400, 288, -1), (1100, 16, 4, 260, 64, 290),
     # the second product's K in one to six blocks of 256, and in more
@@ -283,6 +283,154 @@ def test_expert_ffn(T, E, k, m, d, cap):
     moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q, rt.h_s, rt.out, rt.ws)
     assert torch.equal(rt.out, out)
     assert moe.moe_get_device_status(rt.ws) == 0
+
+
+PAIR_CASES = [
+    # rows enough for the CTA-pair kernels, most of them dropped so that the tiles are ragged:
+    # K of the first product in 1, 2, 4 and more blocks of 256, of the second (A resident) in
+    # 2 to 6, and in more (A streamed)
+    (16000, 5, 4, 500, 96, 333), (16000, 2, 2, 500, 320, 1000), (12000, 3, 3, 360, 800, 300),
+    (6000, 2, 2, 700, 800, 511), (6000, 2, 2, 1000, 800, 700), (4100, 2, 2, 1270, 800, 257),
+    (2300, 2, 2, 1500, 1600, 900), (4100, 2, 2, 1600, 800, 600), (1700, 2, 2, 1000, 2336, -1),
+    # experts in more than one row of 32, and more than 8
+    (12000, 40, 4, 700, 1056, 70), (9000, 12, 2, 1000, 1600, 300),
+]
+
+
+@pytest.mark.parametrize("T,E,k,m,d,cap", PAIR_CASES)
+def test_expert_ffn_pairs(T, E, k, m, d, cap):
+    test_expert_ffn(T, E, k, m, d, cap)
+
+
+@pytest.mark.parametrize("T,m,d", [(40, 64, 128), (8000, 700, 1056)])
+def test_expert_offsets_out_of_range(T, m, d):
+    """Offsets that no dispatch writes are reported; nothing outside the buffers is touched."""
+    g = torch.Generator().manual_seed(T)
+    E, k = 4, 2
+    idx = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    W = _experts(E, m, d, T)[0]
+    rt = _Routed(idx, torch.randn(T, d, generator=g).bfloat16(), E, m)
+    n, guard = T * k * d, 1 << 16
+    big = torch.full((n + 2 * guard,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[guard:guard + n].view(T * k, d)
+    for bad in ([0, T * k // 2, 5, 9, T * k], [-300, 3, 4, T, 2 ** 31 - 1], [T * k + 999] * 5):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for call in (lambda: moe.moe_expert_up_mx4(rt.p, rt.x_q, rt.x_s, off, W, rt.h_q, rt.h_s, rt.ws),
+                     lambda: moe.moe_expert_down_mx4(rt.p, rt.h_q, rt.h_s, off, W, out, rt.ws)):
+            call()
+            assert moe.moe_get_device_status(rt.ws) == moe.MOE_ERR_DEVICE_BADINDEX
+        assert (big[:guard] == 7).all() and (big[guard + n:] == 7).all()
+    # falling offsets count as the largest before them: rows T*k/2.. of expert 3 alone
+    rt.h_q.fill_(0xAA)
+    rt.out.fill_(7.0)
+    off = torch.tensor([0, 0, 0, T * k // 2, T * k // 4], dtype=torch.int32, device="cuda")
+    moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, off, W, rt.h_q, rt.h_s, rt.out, rt.ws)
+    assert moe.moe_get_device_status(rt.ws) == moe.MOE_ERR_DEVICE_BADINDEX
+    assert (rt.out[T * k // 2:] == 7).all() and (rt.h_q.view(T * k, -1)[T * k // 2:] == 0xAA).all()
+    moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q, rt.h_s, rt.out, rt.ws)
+    assert moe.moe_get_device_status(rt.ws) == 0
+
+
+def test_dispatch_slots_out_of_range():
+    """Slots and offsets outside the buffers are skipped."""
+    T, E, k, d = 33, 4, 2, 96
+    p = moe.params(T, d, E, k, 32)
+    nq, ns, pad = moe.moe_mx4_rows_bytes(p, d), moe.moe_mx4_row_scales_bytes(p, d), 1 << 16
+    q = torch.full((nq + 2 * pad,), 0xAA, dtype=torch.uint8, device="cuda")
+    s = torch.full((ns + 2 * pad,), 0xAA, dtype=torch.uint8, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.ones(T, d, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(T, k, **i32)
+    slot = torch.tensor([T * k, T * k + 5, 2 ** 31 - 1, -7, 3], **i32).repeat(14)[: T * k].view(T, k)
+    for off in ([4] * 5, [-9] * 5):  # row 3 lies before its expert's offset, or that below 0
+        moe.moe_mx4_dispatch(p, x, idx, slot.contiguous(), torch.tensor(off, **i32),
+                             q[pad:pad + nq], s[pad:pad + ns])
+        assert (q == 0xAA).all() and (s == 0xAA).all()
+
+
+@pytest.mark.parametrize("T,m,d", [(7, 96, 256), (300, 172, 512), (6000, 500, 800)])
+def test_weights_rewritten_right_before(T, m, d):
+    """Weights quantised on the same stream right before the products, eager and replayed: the
+    second product's early loads read the new ones."""
+    g = torch.Generator().manual_seed(T)
+    E, k = 4, 2
+    m16, m8 = mp.up(m, 16), mp.up(m, 8)
+    idx = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    rt = _Routed(idx, torch.randn(T, d, generator=g).bfloat16(), E, m)
+    ffn = lambda W, out: moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q,
+                                                rt.h_s, out, rt.ws)
+    src, refs = [], []
+    for seed in range(3):
+        gg = torch.Generator(device="cuda").manual_seed(seed)
+        w13 = torch.randn(E, 2 * m16, d, generator=gg, device="cuda").bfloat16()
+        w2 = torch.randn(E, d, m8, generator=gg, device="cuda").bfloat16()
+        W = moe.Mx4Experts.quantize(w13, w2, E, m, d)
+        torch.cuda.synchronize()
+        out = torch.empty_like(rt.out)
+        ffn(W, out)
+        torch.cuda.synchronize()
+        src.append((w13, w2))
+        refs.append(out)
+    w13, w2 = (t.clone() for t in src[0])
+    W = moe.Mx4Experts.quantize(w13, w2, E, m, d)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        def step():
+            moe.moe_mx4_quantize(w13, out=(W.W13_q, W.W13_s))
+            moe.moe_mx4_quantize(w2, out=(W.W2_q, W.W2_s))
+            ffn(W, rt.out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step()
+        for run in (step, graph.replay):
+            for _ in range(4):
+                for (a, b), ref in zip(src, refs):
+                    w13.copy_(a)
+                    w2.copy_(b)
+                    run()
+                    assert torch.equal(rt.out[: rt.R], ref[: rt.R])
+    st.synchronize()
+    assert moe.moe_get_device_status(rt.ws) == 0
+
+
+LIMIT_NS = 2_000_000_000
+
+
+def _cold():
+    """Nothing in L2, so that the first waits are long."""
+    torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,E,m,d", [(40, 2, 96, 512), (2000, 64, 688, 4096), (16000, 8, 1376, 4096)])
+def test_expert_wait_limit(T, E, m, d):
+    """With a wait limit of 0 the products give up at a wait that is not over at its second
+    look (the larger batches have such waits), report it and return: either that or the
+    output is whole.  The next are right."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k = 2
+    idx = torch.rand(T, E, generator=g, device="cuda").argsort(1)[:, :k].cpu()
+    W = moe.Mx4Experts.quantize(
+        torch.randn(E, 2 * mp.up(m, 16), d, generator=g, device="cuda").bfloat16(),
+        torch.randn(E, d, mp.up(m, 8), generator=g, device="cuda").bfloat16(), E, m, d)
+    rt = _Routed(idx, torch.randn(T, d, generator=g, device="cuda").bfloat16(), E, m)
+    ffn = lambda: moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q, rt.h_s,
+                                         rt.out, rt.ws)
+    ffn()
+    ref = rt.out.clone()
+    assert moe.moe_get_device_status(rt.ws) == 0
+    _cold()
+    moe.moe_set_wait_limit_ns(0)
+    try:
+        ffn()
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(LIMIT_NS)
+    status = moe.moe_get_device_status(rt.ws)
+    assert status == moe.MOE_ERR_DEVICE_TIMEOUT or (status == 0 and torch.equal(rt.out, ref))
+    ffn()
+    assert torch.equal(rt.out, ref) and moe.moe_get_device_status(rt.ws) == 0
 
 
 # --------------------------------------------------------------------------- the layer
@@ -468,3 +616,91 @@ def test_layer_graphs_and_streams(act):
                 assert torch.equal(L.run(act).y, ref)
     s.synchronize()
     assert moe.moe_get_device_status(A.ws) == 0
+
+
+def test_layer_few_wait_limit():
+    """The same for the grid barrier of the few-token layer."""
+    L = _Layer(T=8, E=8, k=2, m=344, d=1024)
+    ref = L.run(moe.MX4_ACT_BF16).y.clone()
+    _cold()
+    moe.moe_set_wait_limit_ns(0)
+    try:
+        y = L.run(moe.MX4_ACT_BF16).y
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(LIMIT_NS)
+    status = moe.moe_get_device_status(L.ws)
+    assert status == moe.MOE_ERR_DEVICE_TIMEOUT or (status == 0 and torch.equal(y, ref))
+    for _ in range(3):
+        assert torch.equal(L.run(moe.MX4_ACT_BF16).y, ref)
+    assert moe.moe_get_device_status(L.ws) == 0
+
+
+@pytest.mark.parametrize("mode", [moe.DISJOINT, moe.STACKED])
+def test_partition_quantize_and_serve(mode):
+    """As a server uses them: expert weights from a dense FFN (or stacked experts), quantised
+    once; a prompt through quantised rows, then decode steps with bf16 activations on the same
+    workspace, each compared with moe_forward on the dequantised weights."""
+    E, k, m, d, T = 8, 2, 96, 256, 200
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * 0.06).bfloat16()
+    if mode == moe.DISJOINT:
+        W1, W3, W2 = r(E * m, d), r(E * m, d), r(d, E * m)
+    else:
+        W1, W3, W2 = r(E, m, d), r(E, m, d), r(E, d, m)
+    p = moe.params(T, d, E, k, m, balance_lambda=0.01)
+    ws = moe.Workspace(p)
+    perm = torch.randperm(E * m, generator=g, device="cuda").int() if mode == moe.DISJOINT else None
+    W13_e, W2_e = moe.moe_partition_experts(W1, W3, W2, E, mode=mode, perm=perm, ws=ws)
+    W = moe.Mx4Experts.quantize(W13_e, W2_e, E, m, d)
+    m16, m8 = mp.up(m, 16), mp.up(m, 8)
+    D13 = moe.moe_mx4_dequantize(W.W13_q, W.W13_s, d).reshape(-1)
+    D2 = moe.moe_mx4_dequantize(W.W2_q, W.W2_s, m8).reshape(-1)
+    x, Wg = r(T, d) * 20, r(d, E)
+
+    # the prompt: the layer is its public steps, one by one
+    b = moe.Mx4Buffers(p, act=moe.MX4_ACT_MX4)
+    moe.moe_forward_mx4(p, x, Wg, W, ws, b, act=moe.MX4_ACT_MX4)
+    s = moe.Mx4Buffers(p, act=moe.MX4_ACT_MX4)
+    moe.moe_route(p, x, Wg, None, None, None, ws, s.topk_idx, s.topk_w, s.probs_sum, s.importance)
+    moe.moe_dispatch_rows(p, s.topk_idx, ws, s.row_token, s.slot_row, s.counts, s.kept, s.offsets)
+    moe.moe_mx4_dispatch(p, x, s.topk_idx, s.slot_row, s.offsets, s.x_q, s.x_s)
+    moe.moe_expert_up_mx4(p, s.x_q, s.x_s, s.offsets, W, s.h_q, s.h_s, ws)
+    moe.moe_expert_down_mx4(p, s.h_q, s.h_s, s.offsets, W, s.out, ws)
+    moe.moe_combine(p, s.out, s.slot_row, s.topk_w, s.y)
+    assert torch.equal(b.y, s.y) and torch.equal(b.topk_idx, s.topk_idx)
+
+    # decode steps of every small size: against the same weights in bf16
+    v13 = mp.f64(D13).reshape(E, m16 // 16, 2, 16, d)
+    v1, v3 = (v13[:, :, i].reshape(E, m16, d)[:, :m] for i in (0, 1))
+    v2 = mp.f64(D2).reshape(E, d, m8)[:, :, :m]
+    at = 0
+    for n in (1, 2, 5, 8, 9, 16):
+        q = moe.params(n, d, E, k, m, balance_lambda=0.01)
+        xs = x[at:at + n].contiguous()
+        at += n
+        f = moe.Mx4Buffers(q, act=moe.MX4_ACT_BF16)
+        moe.moe_forward_mx4(q, xs, Wg, W, ws, f)
+        o = moe.ForwardBuffers(q)
+        moe.moe_forward(q, xs, Wg, D13, D2, ws, o)
+        assert torch.equal(f.topk_idx, o.topk_idx) and torch.equal(f.slot_row, o.slot_row)
+        # both round h to bf16 (2^-8 each), moe_forward the expert outputs as well, and y twice
+        X, G, I = mp.f64(xs), mp.f64(f.topk_w), f.topk_idx.cpu().numpy()
+        y, tol = np.zeros((n, d)), np.zeros((n, d))
+        for t in range(n):
+            for j in range(k):
+                e = I[t, j]
+                gate, up = v1[e] @ X[t], v3[e] @ X[t]
+                h = gate / (1 + np.exp(-gate)) * up
+                acc = _acc_bound(d) * ((np.abs(v1[e]) @ np.abs(X[t])) * 1.1 * np.abs(up)
+                                       + (np.abs(v3[e]) @ np.abs(X[t])) * np.abs(h / up))
+                dh = 2 * (2.0 ** -8 + 2.0 ** -20) * np.abs(h) + 2.1 * acc
+                o_ = v2[e] @ h
+                y[t] += G[t, j] * o_
+                tol[t] += G[t, j] * (np.abs(v2[e]) @ (dh + 2 * _acc_bound(m) * np.abs(h))
+                                     + 2.0 ** -8 * np.abs(o_) * 1.1 + 2.0 ** -20 * np.abs(o_))
+        y, tol = y * (E / k if q.rescale else 1), tol * (E / k if q.rescale else 1)
+        tol += 2 * 2.0 ** -8 * (np.abs(y) + tol)
+        assert (np.abs(mp.f64(f.y) - mp.f64(o.y)) <= tol).all()
+        assert (np.abs(mp.f64(f.y) - y) <= tol).all()
+    assert moe.moe_get_device_status(ws) == 0

@@ -187,3 +187,12 @@ def test_buffers_given_by_name():
         moe.Mx4Buffers(p, device="cpu", y=y[:3])
     with pytest.raises(ValueError):
         moe.Mx4Buffers(p, device="cpu", y=y.float())
+
+
+def test_workspace_given():
+    import torch
+    p = moe.params(4, 64, 8, 2, 16)
+    n = moe.moe_workspace_size(p)
+    for buf in (torch.zeros(n - 1, dtype=torch.uint8), torch.zeros(n, dtype=torch.float32)):
+        with pytest.raises(moe.MoeError):
+            moe.Workspace(p, buf=buf)
