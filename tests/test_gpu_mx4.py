@@ -285,7 +285,7 @@ def test_expert_ffn(T, E, k, m, d, cap):
     assert moe.moe_get_device_status(rt.ws) == 0
 
 
-PAIR_CASES = [
+MORE_CASES = [
     # rows enough for the CTA-pair kernels, most of them dropped so that the tiles are ragged:
     # K of the first product in 1, 2, 4 and more blocks of 256, of the second (A resident) in
     # 2 to 6, and in more (A streamed)
@@ -294,11 +294,15 @@ PAIR_CASES = [
     (2300, 2, 2, 1500, 1600, 900), (4100, 2, 2, 1600, 800, 600), (1700, 2, 2, 1000, 2336, -1),
     # experts in more than one row of 32, and more than 8
     (12000, 40, 4, 700, 1056, 70), (9000, 12, 2, 1000, 1600, 300),
+    # nothing kept
+    (9000, 12, 2, 1000, 1600, 0), (64, 4, 2, 64, 96, 0),
+    # one neuron
+    (5, 2, 1, 1, 32, -1),
 ]
 
 
-@pytest.mark.parametrize("T,E,k,m,d,cap", PAIR_CASES)
-def test_expert_ffn_pairs(T, E, k, m, d, cap):
+@pytest.mark.parametrize("T,E,k,m,d,cap", MORE_CASES)
+def test_expert_ffn_more(T, E, k, m, d, cap):
     test_expert_ffn(T, E, k, m, d, cap)
 
 
@@ -392,6 +396,46 @@ def test_weights_rewritten_right_before(T, m, d):
                     assert torch.equal(rt.out[: rt.R], ref[: rt.R])
     st.synchronize()
     assert moe.moe_get_device_status(rt.ws) == 0
+
+
+@pytest.mark.parametrize("T,m,d", [(40, 96, 256), (8000, 700, 1056)])
+def test_expert_ffn_nan_token(T, m, d):
+    """A NaN or an infinity in a token's row stays with that token."""
+    g = torch.Generator().manual_seed(T)
+    E, k = 4, 2
+    idx = torch.rand(T, E, generator=g).argsort(1)[:, :k]
+    W = _experts(E, m, d, T)[0]
+    x = torch.randn(T, d, generator=g).bfloat16()
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[7, 5], x[T - 1, d - 1] = float("nan"), float("-inf")
+        rt = _Routed(idx, x, E, m)
+        moe.moe_expert_ffn_mx4(rt.p, rt.x_q, rt.x_s, rt.offsets, W, rt.h_q, rt.h_s, rt.out, rt.ws)
+        outs.append(rt.out.clone())
+    hit = (rt.row_token == 7) | (rt.row_token == T - 1)
+    assert torch.isnan(outs[1][hit]).all() and int(hit.sum()) == 2 * k
+    assert torch.equal(outs[0][~hit], outs[1][~hit])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each, in flight together."""
+    layers = [_Layer(T=16, E=8, k=2, m=344, d=1024, seed=s) for s in range(2)]
+    acts = (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4)
+    refs = [[L.run(a).y.clone() for a in acts] for L in layers]
+    bufs = [[[moe.Mx4Buffers(L.p, act=a) for _ in range(6)] for a in acts] for L in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    for i in range(6):
+        for n, (L, st) in enumerate(zip(layers, streams)):
+            with torch.cuda.stream(st):
+                for a, b in zip(acts, bufs[n]):
+                    L.run(a, b[i])
+    torch.cuda.synchronize()
+    for n, L in enumerate(layers):
+        for ref, b in zip(refs[n], bufs[n]):
+            assert all(torch.equal(c.y, ref) for c in b)
+        assert moe.moe_get_device_status(L.ws) == 0
 
 
 LIMIT_NS = 2_000_000_000
@@ -524,7 +568,7 @@ FEW_CASES = [
     dict(T=16, E=32, k=8, m=48, d=160, rescale=False), dict(T=16, E=4, k=2, m=40, d=96, cap=0),
     dict(T=5, E=5, k=1, m=1000, d=64), dict(T=13, E=3, k=3, m=72, d=8192),
     dict(T=16, E=2, k=2, m=5000, d=64), dict(T=7, E=12, k=5, m=24, d=4096, noisy=True),
-    dict(T=2, E=24, k=8, m=130, d=736, router=moe.ST),
+    dict(T=2, E=24, k=8, m=130, d=736, router=moe.ST), dict(T=2, E=2, k=1, m=1, d=32),
 ]
 
 
