@@ -195,6 +195,7 @@ cudaError_t launch_mx4_dispatch(const moe_params_t *p, const void *x, const int3
 cudaError_t launch_mx4_up(const moe_params_t *p, const void *xq, const void *xs,
                           const int32_t *offsets, const void *W13q, const void *W13s, void *hq,
                           void *hs, int32_t *status, cudaStream_t s);
+// after_up: the launch before on s is launch_mx4_up with the same offsets
 cudaError_t launch_mx4_down(const moe_params_t *p, const void *hq, const void *hs,
                             const int32_t *offsets, const void *W2q, const void *W2s, void *out,
                             bool after_up, int32_t *status, cudaStream_t s);

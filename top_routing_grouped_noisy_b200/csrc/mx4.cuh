@@ -17,7 +17,6 @@ namespace moe {
 
 constexpr int kMx4Block = 32;      // columns that share a scale
 constexpr int kMx4Tile = 512;      // bytes of a scale tile: 128 rows x 4 blocks
-constexpr uint32_t kInfBits = 0x7f800000u;
 
 // Scale byte (s + 127) of a block whose largest magnitude has the bit pattern `amax`;
 // 255 for a NaN or an infinity.

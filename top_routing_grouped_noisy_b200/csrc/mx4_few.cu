@@ -501,8 +501,8 @@ __device__ __forceinline__ void chunk_mma(float (&sum)[NB][4], uint32_t st, cons
 // --------------------------------------------------------------------- the router
 // The logits lg [T][nout] of all tokens.  A group's warps have the slices of a window of x in
 // registers already (x, of window 0; left holding the last window's); the groups share a
-// slice's 32-column steps, step s to group s % groups.  The warp's rows of [W_g | W_noise] pass through its own `stage` bytes, and
-// the warps' sums (`part`) are added in warp order.
+// slice's 32-column steps, step s to group s % groups.  The warp's rows of [W_g | W_noise] pass
+// through its own `stage` bytes, and the warps' sums (`part`) are added in warp order.
 template <int NB>
 __device__ __forceinline__ void router_logits(const Args &a, const UpPlan &p, uint4 (&x)[NB][8],
                                               char *stage, int stage_bytes, float *part, float *lg)
