@@ -201,6 +201,8 @@ def _check(rc):
 def _p(t):
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.is_cuda and t.is_contiguous():
+        return t.data_ptr() or None
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor, got %r" % type(t))
     if not t.is_cuda:
@@ -213,13 +215,17 @@ def _p(t):
 # the current stream's handle without building a torch.cuda.Stream (3 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None)
+_started = False
 
 
 def _stream(stream=None):
+    global _started
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is None or _device is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
+    if not _started:
+        s = torch.cuda.current_stream().cuda_stream  # starts CUDA
+        _started = _raw_stream is not None and _device is not None
+        return s
     return _raw_stream(_device())
 
 

@@ -22,7 +22,7 @@
 // columns for each stage.  Roles: warp 0 TMA producer, warp 1 TMEM allocator and issuer, warps
 // 2-9 epilogue (each thread one row, half of the columns).
 //
-// Measured (d 4096, m 1376, 8 experts, top 2; a3 / a4): 1 token 7.9 / 5.9 us (weights 11.9 and
+// Measured (d 4096, m 1376, 8 experts, top 2; a3 / a4): 1 token 8.1 / 5.3 us (weights 11.9 and
 // 6.0 MB), 203 tokens 13.8 / 9.3, 16384 tokens 133 / 105 (5.57 and 3.52 PFLOP/s, the pair
 // kernels).
 //
@@ -1386,8 +1386,7 @@ static cudaError_t prepare_device(DevInfo **out)
     if (di.sms == 0) {
         int sms = 0, n = 0;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-            (e = allow_smem_1sm<64>()) != cudaSuccess || (e = allow_smem_1sm<128>()) != cudaSuccess ||
-            (e = allow_smem_1sm<192>()) != cudaSuccess ||
+            (e = allow_smem_1sm<128>()) != cudaSuccess || (e = allow_smem_1sm<192>()) != cudaSuccess ||
             (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_UP>, pair::smem_bytes<EPI_UP>())) !=
                 cudaSuccess ||
             (e = allow_smem(pair::mx4_gemm_2sm_kernel<EPI_DOWN>, pair::smem_bytes<EPI_DOWN>())) !=
@@ -1429,12 +1428,14 @@ static cudaError_t scale_map(CUtensorMap *map, const void *base, uint64_t tk, ui
 // boxes of 32, and B's.  A wave of the pair kernels and their longer start cost as much as the
 // rows below, fitted to times at 1 to 64 experts, 2 to 12000 rows and 1 to 16 stages.  Row
 // tiles are estimated for T*k rows spread evenly over the experts; each ragged end adds half a
-// tile.  Measured (d 4096, m 1376, us; 192 / 128 / 64 / pair):
-//   UP,   8 experts:  16 rows 11 / 13 / 17 / 18; 1024 rows 18 / 16 / 25 / 19;
-//                     2048 rows 21 / 22 / 36 / 20; 8192 rows 53 / 65 / 108 / 42
-//   UP,   1 expert:   200 rows 10 / 8.9 / 8.4 / 11; 1536 rows 17 / 16 / 25 / 12
-//   DOWN, 8 experts:  406 rows 10 / 8.6 / 11 / 12; 2048 rows 17 / 20 / 25 / 18;
-//                     8192 rows 49 / 52 / 74 / 33
+// tile.  Measured (d 4096, m 1376, us; 192 / 128 / pair):
+//   UP,   8 experts:  16 rows 11 / 13 / 18; 1024 rows 18 / 16 / 19; 2048 rows 21 / 22 / 20;
+//                     8192 rows 53 / 65 / 42
+//   UP,   1 expert:   200 rows 10 / 8.9 / 11; 1536 rows 17 / 16 / 12
+//   DOWN, 8 experts:  406 rows 10 / 8.6 / 12; 2048 rows 17 / 20 / 18; 8192 rows 49 / 52 / 33
+// Tiles of 64 columns won where they alone filled one wave, by up to 0.5 us in a product, and
+// lost it in the FFN, where DOWN's loads begin on the SMs that UP leaves free (1 token 13.3 us
+// with both at 64, 12.2 at 128).
 struct Choice {
     bool two;
     int bn;
@@ -1453,7 +1454,7 @@ static Choice choose(const DevInfo &di, int64_t rows, int E, int N, int num_kb, 
     const int start = resident ? 23000 / (15 * num_kb + 38) : 2400 / num_kb;
     const int wave = resident ? 250 + 170 / num_kb : 280;
     int64_t best = (pairs + di.pair_clusters - 1) / di.pair_clusters * wave + start;
-    for (int w : {192, 128, 64}) {
+    for (int w : {192, 128}) {
         const int64_t tiles = row_tiles(BM) * ((N + w - 1) / w);
         const int64_t cost = (tiles + di.sms - 1) / di.sms * (a_rows + w);
         if (cost < best) {
@@ -1502,8 +1503,6 @@ static cudaError_t launch_gemm(const void *A, const void *B, const GemmArgs &arg
             return e;
     }
     if (!two) {
-        if (bn == 64)
-            return launch_1sm<EPI, 64>(*di, ta, tb, to, args, s);
         if (bn == 128)
             return launch_1sm<EPI, 128>(*di, ta, tb, to, args, s);
         return launch_1sm<EPI, 192>(*di, ta, tb, to, args, s);
