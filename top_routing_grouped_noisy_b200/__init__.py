@@ -90,6 +90,8 @@ _MX4_FIELDS = ["x", "Wg", "Wnoise", "noise", "bias", "W13_q", "W13_s", "W2_q", "
                "router_packed", "y", "loss", "counts", "importance", "f", "P", "topk_idx", "topk_w",
                "probs_sum", "row_token", "slot_row", "kept", "offsets", "h", "x_q", "x_s", "h_q",
                "h_s", "out"]
+# the caller's outputs and tables; h of bf16 activations lies between them and these of mx4 ones
+_MX4_OUTPUTS, _MX4_ROWS = _MX4_FIELDS[10:-6], _MX4_FIELDS[-5:]
 
 
 class _Mx4Buffers(C.Structure):
@@ -819,27 +821,12 @@ def moe_mx4_dequantize(codes, scales, K, dtype=torch.bfloat16, out=None, stream=
     return out
 
 
-class _Pointers:
-    """Keeps the device pointers of its tensor attributes up to date as they are set, so that
-    a call need not look at every tensor again."""
-
-    def __init__(self, struct):
-        object.__setattr__(self, "_c", struct)
-
-    def __setattr__(self, name, t):
-        if name in self._names:
-            setattr(self._c, name, _p(t) if t is None or t.is_cuda else None)
-        object.__setattr__(self, name, t)
-
-
-class Mx4Experts(_Pointers):
+class Mx4Experts:
     """The packed expert weights of a layer in mx4: W13_q / W13_s of W13_e [E][2*m16][d] and
-    W2_q / W2_s of W2_e [E][d][m8]."""
-
-    _names = ("W13_q", "W13_s", "W2_q", "W2_s")
+    W2_q / W2_s of W2_e [E][d][m8].  A call reads where its tensors lie at that moment, so they
+    may be set anew or get another storage between calls."""
 
     def __init__(self, W13_q, W13_s, W2_q, W2_s):
-        super().__init__(_Mx4Buffers())
         self.W13_q, self.W13_s, self.W2_q, self.W2_s = W13_q, W13_s, W2_q, W2_s
 
     @classmethod
@@ -858,31 +845,28 @@ def moe_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s, stream=None):
 
 def moe_expert_up_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, ws, stream=None):
     _check(lib().moe_expert_up_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
-                                   W._c.W13_q, W._c.W13_s, _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
+                                   _p(W.W13_q), _p(W.W13_s), _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
                                    _stream(stream)))
 
 
 def moe_expert_down_mx4(p, h_q, h_s, offsets, W: Mx4Experts, out, ws, stream=None):
     _check(lib().moe_expert_down_mx4(C.byref(p), _p(h_q), _p(h_s), _p(offsets),
-                                     W._c.W2_q, W._c.W2_s, _p(out), ws.ptr, ws.nbytes,
+                                     _p(W.W2_q), _p(W.W2_s), _p(out), ws.ptr, ws.nbytes,
                                      _stream(stream)))
 
 
 def moe_expert_ffn_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, out, ws, stream=None):
     _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
-                                    W._c.W13_q, W._c.W13_s, W._c.W2_q, W._c.W2_s, _p(h_q), _p(h_s),
-                                    _p(out), ws.ptr, ws.nbytes, _stream(stream)))
+                                    _p(W.W13_q), _p(W.W13_s), _p(W.W2_q), _p(W.W2_s),
+                                    _p(h_q), _p(h_s), _p(out), ws.ptr, ws.nbytes, _stream(stream)))
 
 
-class Mx4Buffers(_Pointers):
+class Mx4Buffers:
     """Outputs and intermediates of moe_forward_mx4 for layer p, allocated with torch.
     ``act`` limits the intermediates to those of one form (None: both).  A tensor given by
     name (Mx4Buffers(p, y=mine)) is used instead of a new one."""
 
-    _names = tuple(_MX4_FIELDS[10:])
-
     def __init__(self, p: Params, act=None, device="cuda", **given):
-        super().__init__(_Mx4Buffers())
         T, d, E, k, m = p.T, p.d, p.E, p.k, p.m
         rows = T * k
         i32, f32, b16, u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
@@ -898,10 +882,10 @@ class Mx4Buffers(_Pointers):
                 shapes[n + "_q"] = ((moe_mx4_rows_bytes(p, K),), u8)
                 shapes[n + "_s"] = ((moe_mx4_row_scales_bytes(p, K),), u8)
             shapes["out"] = ((rows, d), b16)
-        bad = set(given) - set(self._names)
+        bad = set(given) - set(_MX4_FIELDS[10:])
         if bad:
             raise TypeError("not a buffer of moe_forward_mx4: %s" % ", ".join(sorted(bad)))
-        for n in self._names:
+        for n in _MX4_FIELDS[10:]:
             t = given.get(n)
             if t is None and n in shapes:
                 t = torch.empty(shapes[n][0], dtype=shapes[n][1], device=device)
@@ -918,10 +902,13 @@ def moe_forward_mx4(p, x, Wg, W: Mx4Experts, ws, bufs: Mx4Buffers, act=MX4_ACT_B
                     noise=None, bias=None, router_packed=None, stream=None):
     """The whole layer on mx4 expert weights (include/moe.h): at most 16 tokens with bf16
     activations (MX4_ACT_BF16), or any number with quantised rows (MX4_ACT_MX4)."""
-    b, w = bufs._c, W._c
-    b.x, b.Wg, b.Wnoise, b.noise, b.bias = _p(x), _p(Wg), _p(Wnoise), _p(noise), _p(bias)
-    b.W13_q, b.W13_s, b.W2_q, b.W2_s = w.W13_q, w.W13_s, w.W2_q, w.W2_s
-    b.router_packed = _p(router_packed)
-    _check(lib().moe_forward_mx4(C.byref(p), C.byref(b), int(act), ws.ptr, ws.nbytes,
+    act = int(act)
+    few = act == MX4_ACT_BF16 and p.T > 0
+    b = _Mx4Buffers(_p(x), _p(Wg), _p(Wnoise), _p(noise), _p(bias), _p(W.W13_q), _p(W.W13_s),
+                    _p(W.W2_q), _p(W.W2_s), _p(router_packed),
+                    *[_p(getattr(bufs, n)) for n in _MX4_OUTPUTS],
+                    _p(bufs.h) if few else None,
+                    *[None if few else _p(getattr(bufs, n)) for n in _MX4_ROWS])
+    _check(lib().moe_forward_mx4(C.byref(p), C.byref(b), act, ws.ptr, ws.nbytes,
                                  _stream(stream)))
     return bufs
