@@ -210,3 +210,188 @@ def test_cpu_tensors_refused(rec):
         setattr(owner, name, good)
     L.run()
     assert len(rec.calls) == n + 1
+
+
+def _calls(L, noisy=False):
+    """name, the call, and its tensors by argument: a changed copy of them may be given to it."""
+    p, b, W, i32 = L.p, L.b, L.W, dict(dtype=I32)
+    rows = p.T * p.k
+    t = {n: getattr(b, n) for n in ("topk_idx", "slot_row", "offsets", "x_q", "x_s", "h_q", "h_s",
+                                    "out")}
+    w13 = {n: getattr(W, n) for n in WEIGHTS[:2]}
+    w2 = {n: getattr(W, n) for n in WEIGHTS[2:]}
+    of = lambda a: moe.Mx4Experts(*(a.pop(n, None) for n in WEIGHTS))
+    pick = lambda *ns: {n: t[n] for n in ns}
+
+    def experts_call(fn):
+        def call(a):
+            W = of(a)
+            return fn(p, W=W, ws=L.ws, **a)
+        return call
+
+    yield "dispatch", lambda a: moe.moe_mx4_dispatch(p, **a), \
+        {"x": L.x, **pick("topk_idx", "slot_row", "offsets", "x_q", "x_s")}
+    yield "up", experts_call(moe.moe_expert_up_mx4), \
+        {**pick("x_q", "x_s", "offsets", "h_q", "h_s"), **w13}
+    yield "down", experts_call(moe.moe_expert_down_mx4), \
+        {**pick("h_q", "h_s", "offsets", "out"), **w2}
+    yield "ffn", experts_call(moe.moe_expert_ffn_mx4), \
+        {**pick("x_q", "x_s", "offsets", "h_q", "h_s", "out"), **w13, **w2}
+    more = {"x": L.x, "Wg": L.Wg, "Wnoise": dev(D, E, dtype=BF16), "noise": dev(T, E, dtype=F32),
+            "bias": dev(E, dtype=F32),
+            "router_packed": dev(moe.moe_router_packed_bytes(p, True))}
+    for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+        names = moe._MX4_OUTPUTS + (["h"] if act == moe.MX4_ACT_BF16 else moe._MX4_ROWS)
+
+        def forward(a, act=act, names=names):
+            W, bufs = of(a), copy.copy(b)
+            for n in names:
+                setattr(bufs, n, a.pop(n))
+            return moe.moe_forward_mx4(p, W=W, ws=L.ws, bufs=bufs, act=act, **a)
+
+        yield "forward%d" % act, forward, \
+            {**more, **{n: getattr(b, n) for n in names}, **w13, **w2}
+
+
+def _shorter(t):
+    return t.reshape(-1)[:-1]
+
+
+def _longer(t):
+    return torch.cat([t.reshape(-1), t.reshape(-1)[:1]]).as_subclass(OnDevice)
+
+
+def _other_type(t):
+    return t.to(torch.int16 if t.dtype == BF16 else (F32 if t.dtype == I32 else
+                                                     (I32 if t.dtype == F32 else torch.int8)))
+
+
+def _spaced(t):
+    return torch.stack([t.reshape(-1), t.reshape(-1)], 1).as_subclass(OnDevice)[:, 0]
+
+
+def _elsewhere(t):
+    t = t.clone()
+    t.index = 1
+    return t
+
+
+def _on_host(t):
+    return t.as_subclass(torch.Tensor)
+
+
+def _emptied(t):
+    """A view into a storage that was taken away: data_ptr() is a bare offset."""
+    flat = torch.zeros(t.nbytes + 256, dtype=U8).as_subclass(OnDevice)
+    v = flat[256:].view(t.dtype)
+    flat.untyped_storage().resize_(0)
+    return v
+
+
+REFUSED = {"shorter": _shorter, "type": _other_type, "spaced": _spaced, "device": _elsewhere,
+           "host": _on_host}
+
+
+@pytest.mark.parametrize("how", REFUSED)
+def test_tensors_refused(rec, how):
+    """Too few elements, another type, spaced out, on another device or the host: ValueError
+    before anything is launched, whichever argument it is."""
+    L = Layer()
+    for call_name, call, args in _calls(L):
+        call(dict(args))
+        n = len(rec.calls)
+        for name, t in args.items():
+            if how == "spaced" and t.numel() == 1:
+                continue  # one element is contiguous
+            bad = REFUSED[how](t)
+            with pytest.raises(ValueError):
+                call({**args, name: bad})
+                pytest.fail("%s took %s (%s)" % (call_name, name, how))
+            assert len(rec.calls) == n, (call_name, name)
+
+
+def test_weights_of_another_layer_refused(rec):
+    """Weights have to have the layer's sizes: more bytes are another layout.  Their storage has
+    to be there."""
+    L = Layer()
+    for call_name, call, args in _calls(L):
+        n = len(rec.calls)
+        for name in set(args) & {*WEIGHTS, "Wg", "Wnoise", "bias"}:
+            for bad in (_longer, _emptied):
+                with pytest.raises(ValueError):
+                    call({**args, name: bad(args[name])})
+                    pytest.fail("%s took %s (%s)" % (call_name, name, bad))
+        assert len(rec.calls) == n
+    for W in (experts(m=M - 8), experts(m=2 * M), experts(d=D + 32), experts(E=E + 1)):
+        for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+            with pytest.raises(ValueError, match="W"):
+                L.run(act, W=W)
+    assert len(rec.calls) == n
+
+
+def test_not_a_tensor(rec):
+    L = Layer()
+    for _, call, args in _calls(L):
+        for name in args:
+            for bad in (3, "x", [1.0]):
+                with pytest.raises(TypeError):
+                    call({**args, name: bad})
+
+
+def test_buffers_of_another_batch_refused(rec):
+    """Buffers made for T tokens serve T or fewer."""
+    small, big = Layer(params(T=4)), Layer(params(T=16))
+    n = len(rec.calls)
+    for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+        with pytest.raises(ValueError, match="y: needs at least"):
+            big.run(act, bufs=small.b)
+        with pytest.raises(ValueError):
+            big.run(act, bufs=buffers(params(T=16, d=64)))
+        with pytest.raises(ValueError):
+            big.run(act, bufs=buffers(params(T=16, E=2)))
+    with pytest.raises(ValueError, match="h: needs at least"):
+        big.run(bufs=buffers(params(T=16, m=8)))
+    with pytest.raises(ValueError, match="h_q: needs at least"):
+        big.run(moe.MX4_ACT_MX4, bufs=buffers(params(T=16, m=8)))
+    assert len(rec.calls) == n
+    for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+        small.run(act, bufs=big.b)
+    assert len(rec.calls) == n + 2
+
+
+@pytest.mark.parametrize("act", [moe.MX4_ACT_BF16, moe.MX4_ACT_MX4])
+def test_empty_batch_and_none(rec, act):
+    """T = 0 needs no rows; what is None the library judges."""
+    L = Layer(params(T=0))
+    L.run(act)
+    for n in ("x_q", "x_s", "h_q", "h_s", "out", "y", "topk_idx"):
+        setattr(L.b, n, None)
+    L.run(act)
+    assert rec.struct["x_q"] is None and rec.struct["y"] is None and len(rec.calls) == 2
+
+
+def test_sizes_that_the_library_refuses(monkeypatch):
+    """Sizes outside the contract are the library's to refuse, before it looks at a tensor."""
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: None)
+    x = dev(4, D, dtype=BF16)
+    for p in (params(T=-1), params(E=65), params(m=0), params(k=9)):
+        with pytest.raises(moe.MoeError):
+            moe.moe_mx4_dispatch(p, x, x, x, x, x, x)
+        with pytest.raises(moe.MoeError):
+            moe.moe_expert_down_mx4(p, x, x, x, experts(), x, _Workspace(params()))
+
+
+def test_quantize_other_device(rec):
+    src, codes = dev(2, 3, 64, dtype=F32), dev(2, 3, 32)
+    scales = dev(2, 1, 1, 32, 4, 4)
+    moe.moe_mx4_quantize(src, out=(codes, scales))
+    moe.moe_mx4_dequantize(codes, scales, 64, out=src)
+    n = len(rec.calls)
+    for i in range(3):
+        a = [src, codes, scales]
+        a[i] = _elsewhere(a[i])
+        with pytest.raises(ValueError, match="device 1"):
+            moe.moe_mx4_quantize(a[0], out=(a[1], a[2]))
+        with pytest.raises(ValueError, match="device 1"):
+            moe.moe_mx4_dequantize(a[1], a[2], 64, out=a[0])
+    assert len(rec.calls) == n

@@ -13,6 +13,8 @@ PyTorch provides device memory and streams only.  There is no fallback: if the
 library is missing or a call fails, an exception is raised.
 """
 import ctypes as C
+import functools
+import operator
 import os
 
 import torch
@@ -92,6 +94,8 @@ _MX4_FIELDS = ["x", "Wg", "Wnoise", "noise", "bias", "W13_q", "W13_s", "W2_q", "
                "h_s", "out"]
 # the caller's outputs and tables; h of bf16 activations lies between them and these of mx4 ones
 _MX4_OUTPUTS, _MX4_ROWS = _MX4_FIELDS[10:-6], _MX4_FIELDS[-5:]
+_mx4_few_tensors = operator.attrgetter(*_MX4_OUTPUTS, "h")
+_mx4_row_tensors = operator.attrgetter(*_MX4_OUTPUTS, *_MX4_ROWS)
 
 
 class _Mx4Buffers(C.Structure):
@@ -229,6 +233,13 @@ def _stream(stream=None):
         _started = _raw_stream is not None and _device is not None
         return s
     return _raw_stream(_device())
+
+
+def _current_device():
+    """Index of the current device; -2 before CUDA has started, when no tensor lies on one."""
+    if _started:
+        return _device()
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 def _dtype_code(dt):
@@ -766,6 +777,106 @@ def moe_mx4_row_scales_bytes(p, K) -> int:
     return int(lib().moe_mx4_row_scales_bytes(C.byref(p), K))
 
 
+class _Mx4Needs:
+    """What the mx4 calls take for a layer: for each call a list of (name, type, least bytes) of
+    its tensors, and for the weights the same with their exact bytes (more are another layout)."""
+
+    def __init__(self, p):
+        T, d, E, k, m = p.T, p.d, p.E, p.k, p.m
+        if moe_mx4_rows_bytes(p, d) == 0:  # outside the contract: the library says how
+            _check(lib().moe_mx4_dispatch(C.byref(p), *[None] * 7))
+        u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+        dt, es = (torch.bfloat16, 2) if p.dtype == MOE_BF16 else (f32, 4)
+        m16, m8, rows = (m + 15) // 16 * 16, (m + 7) // 8 * 8, T * k
+        some = min(T, 1)  # an empty batch needs no rows
+        need = dict(
+            x=(dt, T * d * es), Wg=(dt, d * E * es), Wnoise=(dt, d * E * es),
+            noise=(f32, T * E * 4), bias=(f32, E * 4), y=(dt, T * d * es), loss=(f32, 4),
+            counts=(i32, E * 4), importance=(f32, E * 4), f=(f32, E * 4), P=(f32, E * 4),
+            topk_idx=(i32, rows * 4), topk_w=(f32, rows * 4), probs_sum=(f32, E * 4),
+            row_token=(i32, rows * 4), slot_row=(i32, rows * 4), kept=(i32, E * 4),
+            offsets=(i32, (E + 1) * 4), h=(dt, rows * m8 * es), out=(dt, rows * d * es),
+            router_packed=(u8, moe_router_packed_bytes(p, False)))
+        for n, K in (("x", d), ("h", m)):
+            need[n + "_q"] = (u8, some * moe_mx4_rows_bytes(p, K))
+            need[n + "_s"] = (u8, some * moe_mx4_row_scales_bytes(p, K))
+        pick = lambda *names: [(n, *need[n]) for n in names]
+        self.dispatch = pick("x", "topk_idx", "slot_row", "offsets", "x_q", "x_s")
+        self.up = pick("x_q", "x_s", "offsets", "h_q", "h_s")
+        self.down = pick("h_q", "h_s", "offsets", "out")
+        self.ffn = pick("x_q", "x_s", "offsets", "h_q", "h_s", "out")
+        inputs = pick("x", "noise", "router_packed")
+        noisy = inputs[:-1] + [("router_packed", u8, moe_router_packed_bytes(p, True))]
+        # by activations (bf16, mx4) and noise
+        rest = (pick(*_MX4_OUTPUTS, "h"), pick(*_MX4_OUTPUTS, *_MX4_ROWS))
+        self.forward = [[i + r for i in (inputs, noisy)] for r in rest]
+        self.W13 = [("W13_q", u8, E * 2 * m16 * ((d + 31) // 32 * 16)),
+                    ("W13_s", u8, moe_mx4_scales_bytes(E, 2 * m16, d))]
+        self.W2 = [("W2_q", u8, moe_mx4_codes_bytes(E, d, m8)),
+                   ("W2_s", u8, moe_mx4_scales_bytes(E, d, m8))]
+        self.W = self.W13 + self.W2
+        self.all_weights = pick("Wg", "Wnoise", "bias") + self.W
+
+
+@functools.lru_cache(maxsize=256)
+def _mx4_needs_of(params_bytes):
+    return _Mx4Needs(Params.from_buffer_copy(params_bytes))
+
+
+def _mx4_needs(p):
+    return _mx4_needs_of(bytes(p))
+
+
+def _mx4_refuse(t, name, dtype, need, exact):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %r" % (name, type(t)))
+    if not t.is_cuda:
+        raise ValueError("%s: libmoe takes CUDA tensors (got a %s tensor)" % (name, t.device))
+    if t.get_device() != _current_device():
+        raise ValueError("%s: on device %d, the current one is %d"
+                         % (name, t.get_device(), _current_device()))
+    if not t.is_contiguous():
+        raise ValueError("%s: libmoe takes contiguous tensors" % name)
+    raise ValueError("%s: needs %s%d bytes of %s, got %d of %s%s" % (
+        name, "" if exact else "at least ", need, dtype, t.nbytes, t.dtype,
+        ", its storage taken away" if t.untyped_storage().nbytes() < t.nbytes else ""))
+
+
+def _mx4_ptrs(needs, *tensors):
+    """The device pointers of a call's tensors, each compared with what the layer needs: type,
+    bytes, contiguous, on the current device.  None stays NULL, for the library to judge."""
+    dev = _current_device()
+    for t, (name, dtype, least) in zip(tensors, needs):
+        try:
+            if (t.dtype is dtype and t.nbytes >= least and t.get_device() == dev
+                    and t.is_contiguous()):
+                continue
+        except AttributeError:
+            if t is None:
+                continue
+        _mx4_refuse(t, name, dtype, least, False)
+    return [None if t is None else t.data_ptr() or None for t in tensors]
+
+
+def _mx4_weights(needs, *tensors):
+    """The same for weights: exactly the layer's bytes.  Programs take the storage of weights
+    away, to offload or to gather them: data_ptr() is 0 then (NULL), or where the tensor lies
+    inside its storage a bare offset, which is refused here."""
+    dev = _current_device()
+    for t, (name, dtype, n) in zip(tensors, needs):
+        try:
+            if (t.dtype is dtype and t.nbytes == n and t.get_device() == dev
+                    and t.is_contiguous()
+                    and (t.storage_offset() == 0 or t.untyped_storage().nbytes()
+                         >= t.storage_offset() * t.element_size() + n)):
+                continue
+        except AttributeError:
+            if t is None:
+                continue
+        _mx4_refuse(t, name, dtype, n, True)
+    return [None if t is None else t.data_ptr() or None for t in tensors]
+
+
 def _mx4_rows(t):
     """(pointer, G, rows, K, ld) of a matrix or batch of matrices whose columns are
     contiguous and whose rows are evenly spaced through the batch."""
@@ -776,6 +887,9 @@ def _mx4_rows(t):
     ld = b.stride(1) if rows > 1 else (b.stride(0) if G > 1 else K)
     if not t.is_cuda:
         raise ValueError("libmoe takes CUDA tensors (got a %s tensor)" % t.device)
+    if t.get_device() != _current_device():
+        raise ValueError("the matrix is on device %d, the current one is %d"
+                         % (t.get_device(), _current_device()))
     if b.stride(2) != 1 or (G > 1 and b.stride(0) != rows * ld):
         raise ValueError("the rows of the matrices must be contiguous and evenly spaced")
     return t.data_ptr() or None, G, rows, K, ld
@@ -783,13 +897,16 @@ def _mx4_rows(t):
 
 def _mx4_pair(codes, scales, G, rows, K):
     """Pointers of a batch's codes and scales, of the right sizes."""
-    n = G * rows * ((K + 31) // 32 * 16)
-    if codes.dtype != torch.uint8 or codes.numel() != n:
-        raise ValueError("codes must hold %d uint8 elements" % n)
-    n = G * ((rows + 127) // 128) * ((K + 127) // 128) * 512
-    if scales.dtype != torch.uint8 or scales.numel() != n:
-        raise ValueError("scales must hold %d uint8 elements" % n)
-    return _p(codes), _p(scales)
+    out, dev = [], _current_device()
+    for name, t, n in (("codes", codes, G * rows * ((K + 31) // 32 * 16)),
+                       ("scales", scales, G * ((rows + 127) // 128) * ((K + 127) // 128) * 512)):
+        if t.dtype != torch.uint8 or t.numel() != n:
+            raise ValueError("%s must hold %d uint8 elements" % (name, n))
+        ptr = _p(t)
+        if t.get_device() != dev:
+            _mx4_refuse(t, name, torch.uint8, n, True)
+        out.append(ptr)
+    return out
 
 
 def moe_mx4_quantize(src, out=None, stream=None):
@@ -824,7 +941,8 @@ def moe_mx4_dequantize(codes, scales, K, dtype=torch.bfloat16, out=None, stream=
 class Mx4Experts:
     """The packed expert weights of a layer in mx4: W13_q / W13_s of W13_e [E][2*m16][d] and
     W2_q / W2_s of W2_e [E][d][m8].  A call reads where its tensors lie at that moment, so they
-    may be set anew or get another storage between calls."""
+    may be set anew or get another storage between calls, and refuses (ValueError) any that are
+    not of the layer's sizes, uint8, contiguous and on the current device."""
 
     def __init__(self, W13_q, W13_s, W2_q, W2_s):
         self.W13_q, self.W13_s, self.W2_q, self.W2_s = W13_q, W13_s, W2_q, W2_s
@@ -839,32 +957,36 @@ class Mx4Experts:
 
 def moe_mx4_dispatch(p, x, topk_idx, slot_row, offsets, x_q, x_s, stream=None):
     """a2's row copy in mx4 (after moe_dispatch_rows)."""
-    _check(lib().moe_mx4_dispatch(C.byref(p), _p(x), _p(topk_idx), _p(slot_row), _p(offsets),
-                                  _p(x_q), _p(x_s), _stream(stream)))
+    t = _mx4_ptrs(_mx4_needs(p).dispatch, x, topk_idx, slot_row, offsets, x_q, x_s)
+    _check(lib().moe_mx4_dispatch(C.byref(p), *t, _stream(stream)))
 
 
 def moe_expert_up_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, ws, stream=None):
-    _check(lib().moe_expert_up_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
-                                   _p(W.W13_q), _p(W.W13_s), _p(h_q), _p(h_s), ws.ptr, ws.nbytes,
-                                   _stream(stream)))
+    needs = _mx4_needs(p)
+    t = _mx4_ptrs(needs.up, x_q, x_s, offsets, h_q, h_s)
+    t[3:3] = _mx4_weights(needs.W13, W.W13_q, W.W13_s)
+    _check(lib().moe_expert_up_mx4(C.byref(p), *t, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def moe_expert_down_mx4(p, h_q, h_s, offsets, W: Mx4Experts, out, ws, stream=None):
-    _check(lib().moe_expert_down_mx4(C.byref(p), _p(h_q), _p(h_s), _p(offsets),
-                                     _p(W.W2_q), _p(W.W2_s), _p(out), ws.ptr, ws.nbytes,
-                                     _stream(stream)))
+    needs = _mx4_needs(p)
+    t = _mx4_ptrs(needs.down, h_q, h_s, offsets, out)
+    t[3:3] = _mx4_weights(needs.W2, W.W2_q, W.W2_s)
+    _check(lib().moe_expert_down_mx4(C.byref(p), *t, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 def moe_expert_ffn_mx4(p, x_q, x_s, offsets, W: Mx4Experts, h_q, h_s, out, ws, stream=None):
-    _check(lib().moe_expert_ffn_mx4(C.byref(p), _p(x_q), _p(x_s), _p(offsets),
-                                    _p(W.W13_q), _p(W.W13_s), _p(W.W2_q), _p(W.W2_s),
-                                    _p(h_q), _p(h_s), _p(out), ws.ptr, ws.nbytes, _stream(stream)))
+    needs = _mx4_needs(p)
+    t = _mx4_ptrs(needs.ffn, x_q, x_s, offsets, h_q, h_s, out)
+    t[3:3] = _mx4_weights(needs.W, W.W13_q, W.W13_s, W.W2_q, W.W2_s)
+    _check(lib().moe_expert_ffn_mx4(C.byref(p), *t, ws.ptr, ws.nbytes, _stream(stream)))
 
 
 class Mx4Buffers:
     """Outputs and intermediates of moe_forward_mx4 for layer p, allocated with torch.
     ``act`` limits the intermediates to those of one form (None: both).  A tensor given by
-    name (Mx4Buffers(p, y=mine)) is used instead of a new one."""
+    name (Mx4Buffers(p, y=mine)) is used instead of a new one.  A call for another layer than p
+    refuses buffers that are too small for it."""
 
     def __init__(self, p: Params, act=None, device="cuda", **given):
         T, d, E, k, m = p.T, p.d, p.E, p.k, p.m
@@ -904,11 +1026,15 @@ def moe_forward_mx4(p, x, Wg, W: Mx4Experts, ws, bufs: Mx4Buffers, act=MX4_ACT_B
     activations (MX4_ACT_BF16), or any number with quantised rows (MX4_ACT_MX4)."""
     act = int(act)
     few = act == MX4_ACT_BF16 and p.T > 0
-    b = _Mx4Buffers(_p(x), _p(Wg), _p(Wnoise), _p(noise), _p(bias), _p(W.W13_q), _p(W.W13_s),
-                    _p(W.W2_q), _p(W.W2_s), _p(router_packed),
-                    *[_p(getattr(bufs, n)) for n in _MX4_OUTPUTS],
-                    _p(bufs.h) if few else None,
-                    *[None if few else _p(getattr(bufs, n)) for n in _MX4_ROWS])
+    needs = _mx4_needs(p)
+    x, noise, router_packed, *t = _mx4_ptrs(
+        needs.forward[0 if few else 1][0 if Wnoise is None else 1], x, noise, router_packed,
+        *(_mx4_few_tensors if few else _mx4_row_tensors)(bufs))
+    Wg, Wnoise, bias, *w = _mx4_weights(needs.all_weights, Wg, Wnoise, bias, W.W13_q, W.W13_s,
+                                        W.W2_q, W.W2_s)
+    if not few:
+        t.insert(len(_MX4_OUTPUTS), None)  # h
+    b = _Mx4Buffers(x, Wg, Wnoise, noise, bias, *w, router_packed, *t)
     _check(lib().moe_forward_mx4(C.byref(p), C.byref(b), act, ws.ptr, ws.nbytes,
                                  _stream(stream)))
     return bufs
