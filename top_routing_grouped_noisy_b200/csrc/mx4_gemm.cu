@@ -653,13 +653,22 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-// Relaxed: what the arrival hands over is accumulator columns, ordered by tcgen05.wait::ld and
-// the tcgen05 fences.  A release would first wait for this thread's stores of h or of the
-// last output tile, about 700 ns in which no products run.
+// Relaxed: what the arrival hands over is accumulator columns, ordered by hand_over's fence.  A
+// release would first wait for this thread's stores of h or of the last output tile, about
+// 700 ns in which no products run.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
+}
+// The warp hands back the accumulator columns it has loaded so far: every lane's tcgen05.ld (over
+// by tcgen05.wait::ld) is ordered before the arrival by the fence.
+__device__ __forceinline__ void hand_over(uint32_t cluster_addr)
+{
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive_cluster(cluster_addr);
 }
 __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t cluster_addr)
 {
@@ -933,8 +942,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // the shared columns are group 3 of accumulator 0 and group 0 of accumulator 1: the
             // half that has them takes them first
             const bool shares = half == 1 - acc;
-            if (!shares && lane == 0)
-                mbar_arrive_cluster(tfree0);
+            if (!shares)  // for the issuer: this warp has read the tile before
+                hand_over(tfree0);
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
                 const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
@@ -942,12 +951,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                 tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                 tmem_wait_ld();
-                if (shares && i == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_cluster(tfree0);
-                }
+                if (shares && i == 0)
+                    hand_over(tfree0);
                 if constexpr (EPI == EPI_UP) {
                     const int nb = t.n0 / 2 + gi * 32;  // 32 neurons: one block of h
                     uint32_t byte;
@@ -1287,8 +1292,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t taddr =
                     tmem_base + ((uint32_t)lane_base << 16) + (uint32_t)(acc * ACC_STEP);
                 const bool shares = half == 1 - acc;  // as in the kernel above
-                if (!shares && lane == 0)
-                    mbar_arrive_cluster(tfree0);
+                if (!shares)
+                    hand_over(tfree0);
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
                     const int gi = 2 * half + ((acc == 0 && half == 1) ? 1 - i : i);
@@ -1296,12 +1301,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64), v[0]);
                     tmem_ld32_async(taddr + (uint32_t)(gi * 64 + 32), v[1]);
                     tmem_wait_ld();
-                    if (shares && i == 0) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster(tfree0);
-                    }
+                    if (shares && i == 0)
+                        hand_over(tfree0);
                     store_64(a, v, nt * BN + gi * 64, row0, row, u.row_end, st);
                     __syncwarp();  // the next tcgen05.ld takes the whole warp
                 }
