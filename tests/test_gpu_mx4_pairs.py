@@ -44,3 +44,58 @@ def test_many_tiles_in_a_row(m):
         assert torch.equal(rt.out, ref[2])
     side.synchronize()
     assert moe.moe_get_device_status(rt.ws) == 0
+
+
+LIMIT_NS = 2_000_000_000
+
+
+def _runs_out(ws, call, tries=3000):
+    """Whether `call`, with a wait limit of 0 and nothing in L2, reports a wait that ran out.
+    mbarrier.try_wait suspends the thread for some microseconds of its own and a limit is first
+    compared after two of them, so that most waits of a product are over before: of 40 calls, 1
+    to 40 report one, by size.  Calls are repeated until one does."""
+    for _ in range(tries):
+        torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        moe.moe_set_wait_limit_ns(0)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            moe.moe_set_wait_limit_ns(LIMIT_NS)
+        status = moe.moe_get_device_status(ws)
+        assert status in (0, moe.MOE_ERR_DEVICE_TIMEOUT)
+        if status != 0:
+            return True
+    return False
+
+
+# one CTA a tile; pairs, A resident in the second product (m <= 1536); pairs, A streamed
+@pytest.mark.parametrize("T,E,m,d", [(250, 16, 4096, 4096), (16000, 4, 1376, 4096),
+                                     (4000, 2, 4096, 4096)])
+def test_each_product_reports_its_wait(T, E, m, d):
+    """Each product of its own reports MOE_ERR_DEVICE_TIMEOUT when its waits run out, returns, and
+    is right in the next call."""
+    rt, up, down = _batch(T, E, m, d)
+    up()
+    down()
+    ref = rt.h_q.clone(), rt.out.clone()
+    assert moe.moe_get_device_status(rt.ws) == 0
+    for call, buf, want in ((up, rt.h_q, ref[0]), (down, rt.out, ref[1])):
+        assert _runs_out(rt.ws, call)
+        buf.zero_()
+        call()
+        assert torch.equal(buf, want) and moe.moe_get_device_status(rt.ws) == 0
+
+
+def test_few_token_barrier_reports_its_wait():
+    """The same for the grid barrier of the few-token layer: with one expert of 16 neurons all
+    CTAs but one wait there from the start.  The barrier's count serves the next launch."""
+    from test_gpu_mx4 import _Layer
+    L = _Layer(T=1, E=1, k=1, m=16, d=32)
+    ref = L.run(moe.MX4_ACT_BF16).y.clone()
+    for _ in range(3):
+        assert _runs_out(L.ws, lambda: L.run(moe.MX4_ACT_BF16))
+        for _ in range(3):
+            assert torch.equal(L.run(moe.MX4_ACT_BF16).y, ref)
+        assert moe.moe_get_device_status(L.ws) == 0
