@@ -19,7 +19,7 @@
 //             its registers for every item, and the epilogue keeps the routed tokens.
 //   GEMM 2    after a grid barrier (h complete): each CTA owns a strip of at most 32 output
 //             columns.  Column t of B is token t's row of h in the expert at hand; a warp
-//             walks over (expert, 128 columns of h) and adds gate weight * product to the
+//             walks over (expert, 256 columns of h) and adds gate weight * product to the
 //             same sums throughout, so one reduction ends in y.
 //
 // The product.  e2m1 values are exact in f16 (one conversion per pair), so A is the codes
@@ -60,7 +60,23 @@ constexpr int kStrip = 32;                    // GEMM 2: output columns at a tim
 constexpr int kMaxRows = MOE_MX4_FEW_TOKENS * MOE_MAX_TOPK;
 constexpr int kMaxE = 32;
 constexpr int kRegion = 72 * 1024;            // the warps' sums
-constexpr int kSmem = kRegion + kRingBytes;   // dynamic; the static tables take 10 KB
+constexpr int kSmem = kRegion + kRingBytes;   // dynamic; beside it the tables below
+constexpr int kItems = 512;                   // GEMM 1's items at a time
+
+// Routing and work tables of a CTA (static shared memory)
+struct Tables {
+    uint32_t mask[kMaxE];  // tokens that chose an expert
+    int32_t off[kMaxE + 1], sel[kMaxE];
+    int32_t idx[kMaxRows], slot[kMaxRows], rtok[kMaxRows];
+    int8_t map[kMaxE * MOE_MX4_FEW_TOKENS];  // row of (expert, token), -1 none
+    float w[kMaxRows], rw[kMaxRows];
+    float lg[MOE_MX4_FEW_TOKENS * 32], prob[MOE_MX4_FEW_TOKENS * kMaxE], gw[MOE_MX4_FEW_TOKENS * kMaxE];
+    int32_t items[kItems];
+    int abort;
+};
+static_assert(kSmem + sizeof(Tables) <= 227 * 1024, "shared memory of a CTA");
+static_assert(kMaxE * MOE_MX4_FEW_TOKENS == kThreads, "one thread clears an entry of the map");
+static_assert(kMaxRows <= 128 && kMaxRows <= kThreads - 32, "rows in 8 bits; one thread a row");
 
 struct Args {
     const bf16 *x, *Wg, *Wn;
@@ -184,7 +200,6 @@ __device__ __forceinline__ int down_column(int q, int s)
 // --------------------------------------------------------------------- weight rings
 // GEMM 1's items, at most kItems at a time, as a table in shared memory: expert, quads and
 // first quad packed into a word (the divisions behind them are made once per item).
-constexpr int kItems = 512;
 __device__ __forceinline__ int32_t item_pack(int e, int q, int n) { return e | n << 5 | q << 8; }
 __device__ __forceinline__ int item_expert(int32_t v) { return v & 31; }
 __device__ __forceinline__ int item_quads(int32_t v) { return v >> 5 & 7; }
@@ -605,15 +620,7 @@ template <int NB>
 __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_constant__ Args a)
 {
     extern __shared__ __align__(128) char sm[];
-    __shared__ uint32_t s_mask[kMaxE];  // tokens that chose an expert
-    __shared__ int32_t s_off[kMaxE + 1], s_sel[kMaxE];
-    __shared__ int32_t s_idx[kMaxRows], s_slot[kMaxRows], s_rtok[kMaxRows];
-    __shared__ int8_t s_map[kMaxE * MOE_MX4_FEW_TOKENS];  // row of (expert, token), -1 none
-    __shared__ float s_w[kMaxRows], s_rw[kMaxRows];
-    __shared__ float s_lg[MOE_MX4_FEW_TOKENS * 32], s_prob[MOE_MX4_FEW_TOKENS * kMaxE],
-        s_gw[MOE_MX4_FEW_TOKENS * kMaxE];
-    __shared__ int32_t s_items[kItems];
-    __shared__ int s_abort;
+    __shared__ Tables tab;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int T = a.T, E = a.E, k = a.k, d = a.d, m = a.m;
@@ -632,33 +639,33 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     // when the count reaches the next multiple.
     unsigned long long target = 0;
     if (threadIdx.x == kThreads - 1) {
-        s_abort = 0;
+        tab.abort = 0;
         const unsigned long long n = ld_acquire_u64(a.gbar);
         target = (n / gridDim.x + 1) * gridDim.x;
     }
-    s_map[threadIdx.x] = -1;
+    tab.map[threadIdx.x] = -1;
     if (threadIdx.x < kMaxE)
-        s_mask[threadIdx.x] = 0;
+        tab.mask[threadIdx.x] = 0;
 
     // ---- router
     const int nout = a.Wn != nullptr ? 2 * E : E;
     float *part = reinterpret_cast<float *>(region);
-    router_logits<NB>(a, plan, xb, my_ring, 2 * kStageBytes, part, s_lg);
+    router_logits<NB>(a, plan, xb, my_ring, 2 * kStageBytes, part, tab.lg);
     if (warp < T)
-        gate_token_warp(s_lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
+        gate_token_warp(tab.lg + warp * nout, E, k, a.Wn != nullptr ? 1 : 0,
                         a.noise + (a.noise != nullptr ? (size_t)warp * E : 0), a.bias, a.router_type,
-                        s_idx + warp * k, s_w + warp * k, s_prob + warp * E, s_gw + warp * E,
+                        tab.idx + warp * k, tab.w + warp * k, tab.prob + warp * E, tab.gw + warp * E,
                         a.status);
     __syncwarp();
-    if (warp < T && lane < k && s_idx[warp * k + lane] >= 0)
-        atomicOr(&s_mask[s_idx[warp * k + lane]], 1u << warp);
+    if (warp < T && lane < k && tab.idx[warp * k + lane] >= 0)
+        atomicOr(&tab.mask[tab.idx[warp * k + lane]], 1u << warp);
     __syncthreads();
-    // ---- dispatch tables (stable by token, assignments past the capacity dropped).  s_mask[e]
+    // ---- dispatch tables (stable by token, assignments past the capacity dropped).  tab.mask[e]
     // has a bit for each token that chose expert e, so a row's rank is a population count and
     // every warp makes the experts' tables for itself (all write the same values).
     int nsel;
     {
-        const uint32_t chosen = lane < E ? s_mask[lane] : 0u;
+        const uint32_t chosen = lane < E ? tab.mask[lane] : 0u;
         const int cnt = __popc(chosen), kept = a.C < 0 ? cnt : min(cnt, a.C);
         int off = kept;  // inclusive prefix sum
 #pragma unroll
@@ -669,29 +676,29 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         const uint32_t used = __ballot_sync(0xffffffffu, kept > 0);
         nsel = __popc(used);
         if (lane < E) {
-            s_off[lane + 1] = off;
+            tab.off[lane + 1] = off;
             if (lane == 0)
-                s_off[0] = 0;
+                tab.off[0] = 0;
             if (kept > 0)
-                s_sel[__popc(used & ((1u << lane) - 1))] = lane;
+                tab.sel[__popc(used & ((1u << lane) - 1))] = lane;
         }
         // warp t: the rows of token t
-        const int e = warp < T && lane < k ? s_idx[warp * k + lane] : -1;
+        const int e = warp < T && lane < k ? tab.idx[warp * k + lane] : -1;
         const int first = __shfl_sync(0xffffffffu, off - kept, max(e, 0));
         const int room = __shfl_sync(0xffffffffu, kept, max(e, 0));
         if (warp < T && lane < k) {
-            const int rank = e < 0 ? 0 : __popc(s_mask[e] & ((1u << warp) - 1));
+            const int rank = e < 0 ? 0 : __popc(tab.mask[e] & ((1u << warp) - 1));
             const int row = e >= 0 && rank < room ? first + rank : -1;
-            s_slot[warp * k + lane] = row;
+            tab.slot[warp * k + lane] = row;
             if (row >= 0) {
-                s_rtok[row] = warp;
-                s_rw[row] = s_w[warp * k + lane];
-                s_map[e * MOE_MX4_FEW_TOKENS + warp] = (int8_t)row;
+                tab.rtok[row] = warp;
+                tab.rw[row] = tab.w[warp * k + lane];
+                tab.map[e * MOE_MX4_FEW_TOKENS + warp] = (int8_t)row;
             }
         }
         __syncwarp();
     }
-    const int R = s_off[E], m8 = round_up(m, 8);
+    const int R = tab.off[E], m8 = round_up(m, 8);
     const Place place;
     uint32_t a_off[4];  // this lane's words of A row g in a chunk
 #pragma unroll
@@ -717,12 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             for (int j = lane; j < plan.n; j += 32) {  // every warp for itself, the same values
                 int is, q, n;
                 up.get(base + j, is, q, n);
-                s_items[j] = item_pack(s_sel[is], q, n);
+                tab.items[j] = item_pack(tab.sel[is], q, n);
             }
             __syncwarp();
             UpWalk ld(plan);
             if (ld.on(plan)) {
-                up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s, place);
+                up_fill(a, tab.items[ld.i], plan.column(ld.w), ring_s, place);
                 ld.next(plan);
             }
             uint32_t st = 0;
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                     for (int i = b0 + plan.group(); i < b1; i += plan.groups()) {
                         __syncwarp();  // the other stage has been read
                         if (ld.on(plan)) {
-                            up_fill(a, s_items[ld.i], plan.column(ld.w), ring_s + (st ^ kStageBytes), place);
+                            up_fill(a, tab.items[ld.i], plan.column(ld.w), ring_s + (st ^ kStageBytes), place);
                             ld.next(plan);
                         } else {
                             cp_commit();
@@ -786,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
 #pragma unroll 1
                 for (int j = warp; j < (b1 - b0) * 2 * NB; j += kWarps) {
                     const int i = j / (2 * NB), hb = j % (2 * NB);
-                    const int32_t item = s_items[b0 + i];
+                    const int32_t item = tab.items[b0 + i];
                     const float4 *r = reinterpret_cast<const float4 *>(sums) +
                                       (size_t)((i << plan.kshift) * 2 * NB + hb) * 32 + lane;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -796,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                         v = make_float4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
                     }
                     const int s = hb / NB * 8 + g, nrn = up_neuron(item_first(item), s);
-                    const int8_t *map = s_map + item_expert(item) * MOE_MX4_FEW_TOKENS + hb % NB * 8 + 2 * c;
+                    const int8_t *map = tab.map + item_expert(item) * MOE_MX4_FEW_TOKENS + hb % NB * 8 + 2 * c;
                     if (s < 4 * item_quads(item) && nrn < m) {
                         // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
                         if (map[0] >= 0)
@@ -821,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     const DownPlan down(a, nsel);
     DownWalk ld(down);
     if (ld.on(down)) {
-        down_fill(a, down, ld.strip, s_sel[ld.is], ld.u * kSlice, ring_s, place);
+        down_fill(a, down, ld.strip, tab.sel[ld.is], ld.u * kSlice, ring_s, place);
         ld.next(down);
     }
     if (threadIdx.x == kThreads - 1) {
@@ -833,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             t0 = t0 == 0 ? now : t0;
             if (now - t0 > a.wait_ns) {
                 set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-                s_abort = 1;
+                tab.abort = 1;
                 break;
             }
         }
@@ -841,24 +848,24 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
         constexpr int nt = kThreads - 32;
         const int t1 = (int)threadIdx.x;
         if (t1 < T * k) {
-            a.idx[t1] = s_idx[t1];
-            a.w[t1] = s_w[t1];
-            a.slot_row[t1] = s_slot[t1];
+            a.idx[t1] = tab.idx[t1];
+            a.w[t1] = tab.w[t1];
+            a.slot_row[t1] = tab.slot[t1];
         }
         if (t1 < R)
-            a.row_token[t1] = s_rtok[t1];
+            a.row_token[t1] = tab.rtok[t1];
         if (t1 <= E)
-            a.offsets[t1] = s_off[t1];
+            a.offsets[t1] = tab.off[t1];
         // the gate statistics, in gate_stats_kernel's arithmetic
         if (t1 < E) {
             float sp = 0.f, sg = 0.f;
             for (int t = 0; t < T; ++t) {
-                sp += s_prob[t * E + t1];
-                sg += s_gw[t * E + t1];
+                sp += tab.prob[t * E + t1];
+                sg += tab.gw[t * E + t1];
             }
-            const int cnt = __popc(s_mask[t1]);
+            const int cnt = __popc(tab.mask[t1]);
             a.counts[t1] = cnt;
-            a.kept[t1] = s_off[t1 + 1] - s_off[t1];
+            a.kept[t1] = tab.off[t1 + 1] - tab.off[t1];
             a.probs_sum[t1] = sp;
             a.importance[t1] = sg;
             a.f[t1] = (float)((double)cnt / ((double)T * k));
@@ -869,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
             for (int e = 0; e < E; ++e) {
                 float sp = 0.f;
                 for (int t = 0; t < T; ++t)
-                    sp += s_prob[t * E + e];
-                sfp += ((double)__popc(s_mask[e]) / ((double)T * k)) * ((double)sp / (double)T);
+                    sp += tab.prob[t * E + e];
+                sfp += ((double)__popc(tab.mask[e]) / ((double)T * k)) * ((double)sp / (double)T);
             }
             a.loss[0] = (float)(a.lambda * sfp);
         }
@@ -878,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
     __syncthreads();
 
     // ---- GEMM 2 and the combine of this CTA's columns
-    if (!s_abort) {
+    if (!tab.abort) {
         uint32_t st = 0;
 #pragma unroll 1
         for (int strip = 0; strip < down.strips; ++strip) {
@@ -900,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 if (is >= nsel)
                     break;
                 // column t of B: token t's row of this expert, zeros if it has none
-                const int8_t *map = s_map + s_sel[is] * MOE_MX4_FEW_TOKENS;
+                const int8_t *map = tab.map + tab.sel[is] * MOE_MX4_FEW_TOKENS;
                 const bf16 *src[NB];
                 float w[NB], f[NB][2][2];
                 bool on[NB][2];
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 for (int nb = 0; nb < NB; ++nb) {
                     const int row = map[nb * 8 + g];
                     src[nb] = row >= 0 ? a.h + (int64_t)row * m8 : nullptr;
-                    w[nb] = row >= 0 ? s_rw[row] : 0.f;
+                    w[nb] = row >= 0 ? tab.rw[row] : 0.f;
                     // 0 * sum would not do: a NaN weight stays with its tokens
                     on[nb][0] = map[nb * 8 + 2 * c] >= 0;
                     on[nb][1] = map[nb * 8 + 2 * c + 1] >= 0;
@@ -917,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                 load_b<NB, true>(src, u * kSlice, m, x);
                 __syncwarp();  // the other stage has been read
                 if (ld.on(down)) {
-                    down_fill(a, down, ld.strip, s_sel[ld.is], ld.u * kSlice, ring_s + (st ^ kStageBytes),
+                    down_fill(a, down, ld.strip, tab.sel[ld.is], ld.u * kSlice, ring_s + (st ^ kStageBytes),
                               place);
                     ld.next(down);
                 } else {
