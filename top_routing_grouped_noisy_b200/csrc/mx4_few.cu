@@ -4,11 +4,14 @@
 // Mixtral and ST types); capacity: its "容量因子"; SwiGLU expert: "LLaMA-MoE v2", code
 // sample, class Expert; statistics: "LLaMA-MoE v2", section "门控机制设计".
 //
-// The selected experts' weights (0.53 bytes each) are all it has to read; the integer pipe (the
-// conversions of their codes) and the chain routing -> GEMM 1 -> grid barrier -> GEMM 2 take
-// longer.  Measured (d 4096, graph replays): 1 token of 8 experts x 1376, top 2, 18.5 us (18.2 MB,
-// 0.98 TB/s), 8 tokens 33.5 us (65 MB, 1.9 TB/s), 16 tokens of 16 x 688, top 4, 55.7 us (71 MB,
-// 1.3 TB/s).
+// The selected experts' weights (0.53 bytes each) are all it has to read; the chain routing ->
+// GEMM 1 -> grid barrier -> GEMM 2 takes longer, and no unit is full on the way (8 tokens: issue
+// slots 43 %, integer pipe 39 %, tensor pipe 12 %, DRAM 19 %).  Its 4 warps a scheduler wait: of the
+// 9.2 cycles between two instructions of a warp 2.2 are for the next instruction to be fetched (3.3
+// of 11 at 1 token), 1.2 for the result of the last, 1.0 for the pipes, 0.9 at barriers (2.0), 0.6
+// for global loads.  Measured (d 4096, graph replays, weights in L2 / after 512 MB of other reads):
+// 1 token of 8 experts x 1376, top 2, 18.4 / 24.7 us (18.2 MB), 8 tokens 30.7 to 34 / 41 to 44 us
+// (65 MB), 16 tokens of 16 x 688, top 4, 53.3 to 57 / 67 us (71 MB); ranges over inputs.
 //
 //   routing   every CTA computes all logits (mma.sync on bf16), gates and tables: x and W_g
 //             are some ten KB and no CTA waits for another.
@@ -32,9 +35,9 @@
 //
 // Weights stream through two stages of 32 rows x 256 columns with their 64 scale words, which
 // each warp fills for itself with cp.async, one stage ahead and across items: no barrier
-// between loads and products but __syncwarp.  The loop is bound by the integer pipe (the
-// conversions) and by the load unit's lines and wavefronts: B stays in registers (it never
-// passes through shared memory), a copy instruction covers whole 128-byte lines of 4 rows, and
+// between loads and products but __syncwarp.  The loop's work is the conversions (integer pipe)
+// and the load unit's lines and wavefronts: B stays in registers (it never passes through
+// shared memory), a copy instruction covers whole 128-byte lines of 4 rows, and
 // rows are enumerated in the order of the scale tiles -- 4 rows that lie 32 apart share 16
 // bytes of scales -- so that one copy instruction brings all scales of a stage.  Partial sums
 // meet in shared memory in warp order, so results do not depend on timing.
@@ -805,7 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_few_kernel(const __grid_const
                     const int s = hb / NB * 8 + g, nrn = up_neuron(item_first(item), s);
                     const int8_t *map = tab.map + item_expert(item) * MOE_MX4_FEW_TOKENS + hb % NB * 8 + 2 * c;
                     if (s < 4 * item_quads(item) && nrn < m) {
-                        // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit)
+                        // approximate division (2 ulp, 0 once 1 + e^-g > 2^126, silu's limit).
+                        // h is bf16 as moe_forward's h is, a buffer that callers read: half the
+                        // bytes through L2, and y off by 2.4e-3 (rms, of its 64-bit value)
+                        // where its own rounding alone makes 1.7e-3
                         if (map[0] >= 0)
                             a.h[(int64_t)map[0] * m8 + nrn] =
                                 __float2bfloat16_rn(__fdividef(v.x, 1.0f + __expf(-v.x)) * v.z);

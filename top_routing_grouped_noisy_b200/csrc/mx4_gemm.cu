@@ -23,8 +23,9 @@
 // 2-9 epilogue (each thread one row, half of the columns).
 //
 // Measured (d 4096, m 1376, 8 experts, top 2; a3 / a4): 1 token 8.1 / 5.3 us (weights 11.9 and
-// 6.0 MB), 203 tokens 13.8 / 9.3, 16384 tokens 133 / 105 (5.57 and 3.52 PFLOP/s, the pair
-// kernels).
+// 6.0 MB), 203 tokens 13.8 / 9.3, 2048 tokens 25.5 / 25.7, 16384 tokens (the pair kernels) 132 /
+// 108 in a short run (5.6 and 3.4 PFLOP/s) and 154 / 116 in a long one, under the power cap at
+// 1455 / 1690 MHz.
 //
 // Every mbarrier wait is bounded: past the limit the kernel records
 // MOE_ERR_DEVICE_TIMEOUT, stops every role, drains its copies and products (bounded
@@ -585,8 +586,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // 128) of A and of B with A's scales for its rows and B's for all 256 (every CTA's
 // accumulators see all columns); the leader issues M = 256 products.  The 1-SM kernel copies 320
 // rows for 128 x 192 x 256 of work; here 256 rows serve 128 x 256 x 256 of each SM's.
-// A product of 256 x 256 x 64 takes 118 cycles; 5.57 PFLOP/s at 16384 tokens are 84% of four
-// times the measured bf16 rate.
+// UP of 16384 tokens: 5.6 PFLOP/s in a short run, 84% of four times the measured bf16 rate; in a
+// long one 154 us x 1455 MHz (sampled) = 224 thousand cycles for the 1250 products of 256 x 256 x 64
+// that a pair issues, 180 each, where 16384 multiply-adds a cycle and SM would take 128.
 //
 // TMEM.  Two 256-column accumulators do not leave room for scales, so they share 64 columns:
 // accumulator 0 is columns 0..255, accumulator 1 columns 192..447, scales 448..471 and 480..503
