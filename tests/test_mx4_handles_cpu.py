@@ -303,6 +303,8 @@ def test_tensors_refused(rec, how):
         for name, t in args.items():
             if how == "spaced" and t.numel() == 1:
                 continue  # one element is contiguous
+            if how == "type" and name == "router_packed":
+                continue  # moe_router_pack fills a buffer of any type
             bad = REFUSED[how](t)
             with pytest.raises(ValueError):
                 call({**args, name: bad})
@@ -395,3 +397,33 @@ def test_quantize_other_device(rec):
         with pytest.raises(ValueError, match="device 1"):
             moe.moe_mx4_dequantize(a[1], a[2], 64, out=a[0])
     assert len(rec.calls) == n
+
+
+def test_router_packed_of_any_type(rec):
+    """moe_router_pack fills the buffer it is given, whatever its type; so is it taken."""
+    L = Layer()
+    n = moe.moe_router_packed_bytes(L.p, False)
+    for dtype in (U8, BF16, F32):
+        t = dev(n // dtype.itemsize, dtype=dtype)
+        L.run(moe.MX4_ACT_MX4, router_packed=t)
+        assert rec.struct["router_packed"] == t.data_ptr()
+        with pytest.raises(ValueError):
+            L.run(moe.MX4_ACT_MX4, router_packed=t[1:].clone())
+
+
+def test_f32_layers_are_the_librarys_to_refuse(monkeypatch):
+    """With the tensors of a bf16 layer the error is that of the library, not one of sizes."""
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    L = Layer()
+    p32 = params(dtype=moe.MOE_F32)
+    L.ws = _Workspace(p32)
+    L.p = p32
+    for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+        with pytest.raises(moe.MoeError, match="bf16"):
+            L.run(act)
+    x = dev(T, D, dtype=F32)  # the dispatch takes them
+    L.p = params(T=0, dtype=moe.MOE_F32)
+    moe.moe_mx4_dispatch(L.p, x[:0], L.b.topk_idx, L.b.slot_row, L.b.offsets, L.b.x_q, L.b.x_s)
+    with pytest.raises(ValueError, match="x: needs"):
+        moe.moe_mx4_dispatch(p32, L.x, L.b.topk_idx, L.b.slot_row, L.b.offsets, L.b.x_q, L.b.x_s)

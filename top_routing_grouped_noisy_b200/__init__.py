@@ -786,7 +786,7 @@ class _Mx4Needs:
         if moe_mx4_rows_bytes(p, d) == 0:  # outside the contract: the library says how
             _check(lib().moe_mx4_dispatch(C.byref(p), *[None] * 7))
         u8, i32, f32 = torch.uint8, torch.int32, torch.float32
-        dt, es = (torch.bfloat16, 2) if p.dtype == MOE_BF16 else (f32, 4)
+        dt, es = torch.bfloat16, 2  # the library refuses other layers, but for the dispatch
         m16, m8, rows = (m + 15) // 16 * 16, (m + 7) // 8 * 8, T * k
         some = min(T, 1)  # an empty batch needs no rows
         need = dict(
@@ -801,7 +801,8 @@ class _Mx4Needs:
             need[n + "_q"] = (u8, some * moe_mx4_rows_bytes(p, K))
             need[n + "_s"] = (u8, some * moe_mx4_row_scales_bytes(p, K))
         pick = lambda *names: [(n, *need[n]) for n in names]
-        self.dispatch = pick("x", "topk_idx", "slot_row", "offsets", "x_q", "x_s")
+        self.dispatch = pick("x") if p.dtype == MOE_BF16 else [("x", f32, T * d * 4)]
+        self.dispatch += pick("topk_idx", "slot_row", "offsets", "x_q", "x_s")
         self.up = pick("x_q", "x_s", "offsets", "h_q", "h_s")
         self.down = pick("h_q", "h_s", "offsets", "out")
         self.ffn = pick("x_q", "x_s", "offsets", "h_q", "h_s", "out")
@@ -1026,6 +1027,9 @@ def moe_forward_mx4(p, x, Wg, W: Mx4Experts, ws, bufs: Mx4Buffers, act=MX4_ACT_B
     activations (MX4_ACT_BF16), or any number with quantised rows (MX4_ACT_MX4)."""
     act = int(act)
     few = act == MX4_ACT_BF16 and p.T > 0
+    if (isinstance(router_packed, torch.Tensor) and router_packed.dtype is not torch.uint8
+            and router_packed.is_contiguous()):  # moe_router_pack fills a buffer of any type
+        router_packed = router_packed.view(torch.uint8)
     needs = _mx4_needs(p)
     x, noise, router_packed, *t = _mx4_ptrs(
         needs.forward[0 if few else 1][0 if Wnoise is None else 1], x, noise, router_packed,
