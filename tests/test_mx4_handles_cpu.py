@@ -427,3 +427,30 @@ def test_f32_layers_are_the_librarys_to_refuse(monkeypatch):
     moe.moe_mx4_dispatch(L.p, x[:0], L.b.topk_idx, L.b.slot_row, L.b.offsets, L.b.x_q, L.b.x_s)
     with pytest.raises(ValueError, match="x: needs"):
         moe.moe_mx4_dispatch(p32, L.x, L.b.topk_idx, L.b.slot_row, L.b.offsets, L.b.x_q, L.b.x_s)
+
+
+def test_workspace_replaced(monkeypatch):
+    """The workspace's size is that of its buffer at the call: with a smaller buffer in its place
+    the call is refused."""
+    class Init:  # the library but for moe_workspace_init, which needs a device
+        def __getattr__(self, name):
+            return getattr(real, name) if name != "moe_workspace_init" else lambda *a: moe.MOE_OK
+
+    real, init = moe.lib(), Init()
+    monkeypatch.setattr(moe, "lib", lambda: init)
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    L = Layer()
+    n = moe.moe_workspace_size(L.p)
+    for buf in (None, dev(n + 512)):
+        ws = moe.Workspace(L.p, buf=buf if buf is not None else dev(n))
+        assert ws.nbytes == ws.buf.numel()
+        ws.buf = dev(n - 256)
+        assert ws.nbytes == n - 256
+        for act in (moe.MX4_ACT_BF16, moe.MX4_ACT_MX4):
+            with pytest.raises(moe.MoeError, match="workspace"):
+                L.run(act, ws=ws)
+        ws.buf = dev(n)
+        ws.buf.data = torch.zeros(n // 2, dtype=U8)
+        with pytest.raises(moe.MoeError, match="workspace"):
+            L.run(ws=ws)

@@ -304,15 +304,17 @@ class Workspace:
         if buf is not None:
             if buf.dtype != torch.uint8 or buf.numel() < n:
                 raise MoeError(MOE_ERR_WORKSPACE, "the workspace needs %d uint8 elements" % n)
-            n = buf.numel()
         self.buf = buf if buf is not None else torch.empty(n, dtype=torch.uint8,
                                                            device=device or "cuda")
-        self.nbytes = n
-        _check(lib().moe_workspace_init(_p(self.buf), n, _stream()))
+        _check(lib().moe_workspace_init(_p(self.buf), self.nbytes, _stream()))
 
     @property
     def ptr(self):
         return self.buf.data_ptr()
+
+    @property
+    def nbytes(self):
+        return self.buf.nbytes
 
 
 def moe_get_device_status(ws: Workspace, clear=True, stream=None) -> int:
